@@ -105,6 +105,36 @@ static zha_status make_geom(const zha_config* c, zha::Geom* g, size_t* bytes) {
   return ZHA_OK;
 }
 
+zha_status zha_geometry(const zha_config* cfg, zha::Geom* g) { return make_geom(cfg, g, nullptr); }
+zha_status zha_report_cuda(cudaError_t e, const char* who) { return cuda_fail(e, who); }
+
+zha_status zha_batch_view(const zha::Geom& G, const zha_kv_cache* kv, int32_t n_seqs, int64_t max_tokens,
+                          const char* who, zha::KvView* out) {
+  if (kv == nullptr) return fail(ZHA_ERR_INVALID, "%s: cache is NULL", who);
+  if (kv->k == nullptr || kv->v == nullptr || !aligned(kv->k, 16) || !aligned(kv->v, 16))
+    return fail(ZHA_ERR_INVALID, "%s: K and V must be non-NULL 16-byte aligned device pointers", who);
+  if (n_seqs < 1 || n_seqs > 65535) return fail(ZHA_ERR_INVALID, "%s: n_seqs must be 1..65535", who);
+  if (kv->ld < 1) return fail(ZHA_ERR_INVALID, "%s: ld must be >= 1", who);
+  const bool paged = kv->block_table != nullptr;
+  if (paged && (!aligned(kv->block_table, 4) || kv->max_blocks < 1))
+    return fail(ZHA_ERR_INVALID, "%s: the block table needs max_blocks >= 1 entries per KV head", who);
+  constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
+  const int64_t per = paged ? G.chunk : int64_t(n_seqs) * G.hkv;
+  if (kv->ld > kMaxRows / per)
+    return fail(ZHA_ERR_UNSUPPORTED, "%s: more than 2^31 - 512 token slots in the cache", who);
+  if (paged && kv->max_blocks > kMaxRows)
+    return fail(ZHA_ERR_UNSUPPORTED, "%s: max_blocks out of range", who);
+  if (max_tokens < 0 || max_tokens > kMaxRows || max_tokens > (paged ? kv->max_blocks * G.chunk : kv->ld))
+    return fail(ZHA_ERR_INVALID, "%s: max_tokens %lld outside [0, ld or max_blocks * C]", who,
+                (long long)max_tokens);
+  out->k = kv->k;
+  out->v = kv->v;
+  out->ld = kv->ld;
+  out->table = kv->block_table;
+  out->max_blocks = paged ? kv->max_blocks : 0;
+  return ZHA_OK;
+}
+
 extern "C" {
 
 int32_t zha_abi_version(void) { return ZHA_ABI_VERSION; }

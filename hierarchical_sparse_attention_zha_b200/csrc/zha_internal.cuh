@@ -87,6 +87,19 @@ __host__ __device__ inline int64_t kv_row(const KvView& kv, int g, int64_t tok, 
   return int64_t(page) * chunk + (tok - c * chunk);
 }
 
+// Row of token `tok` of KV head g of sequence `seq` in a batch of caches (see
+// zha_attend_batch_kv), or -1. Rows fit 31 bits (checked on the host).
+__host__ __device__ inline int32_t kv_batch_row(const KvView& kv, int hkv, int seq, int g, int64_t tok,
+                                                int chunk) {
+  const int64_t head = int64_t(seq) * hkv + g;
+  if (kv.table == nullptr) return int32_t(head * kv.ld + tok);
+  const int64_t c = tok / chunk;
+  if (c >= kv.max_blocks) return -1;
+  const int32_t page = kv.table[head * kv.max_blocks + c];
+  if (page < 0 || int64_t(page) >= kv.ld) return -1;
+  return int32_t(int64_t(page) * chunk + (tok - c * chunk));
+}
+
 // C^l, saturating at a value above any token count.
 __host__ __device__ inline int64_t span_of(int32_t chunk, int32_t level) {
   int64_t s = 1;
@@ -377,3 +390,10 @@ zha_status zha_check_route_args(const zha_tree* tree, const float* d_Q, int32_t 
                                 int64_t n_tokens, const int32_t* d_chunk_ids,
                                 const int32_t* d_n_chunks, int32_t max_sel, const char* who);
 zha_status zha_check_p(float p, const char* who);
+
+// A configuration's geometry; a batch of caches checked against it (rows in
+// total and per sequence, alignment) as the kernels see it.
+zha_status zha_geometry(const zha_config* cfg, zha::Geom* g);
+zha_status zha_batch_view(const zha::Geom& g, const zha_kv_cache* kv, int32_t n_seqs, int64_t max_tokens,
+                          const char* who, zha::KvView* out);
+zha_status zha_report_cuda(cudaError_t e, const char* who);

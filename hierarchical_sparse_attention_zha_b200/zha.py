@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, byref, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
+from ctypes import POINTER, byref, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 import torch
 
@@ -29,6 +29,9 @@ ZHA_DEV_SELECTION_TRUNCATED = 1
 ZHA_DEV_BAD_SELECTION = 2
 ZHA_DEV_TIMEOUT = 4
 ZHA_DEV_BAD_PAGE = 8
+ZHA_DEV_BAD_LENGTH = 16
+ZHA_DEV_NO_PAGES = 32
+ZHA_DEV_BAD_SEQUENCE = 64
 
 
 class ZhaError(RuntimeError):
@@ -64,6 +67,9 @@ def top_k_policy(k_by_level) -> RoutePolicy:
     return pol
 
 
+_DTYPE = {torch.float32: ZHA_F32, torch.bfloat16: ZHA_BF16}
+
+
 class KvCache(ctypes.Structure):
     """zha_kv_cache: a contiguous [Hkv, ld, d] cache, or page pools [n_pages, C, d]
     with a block table [Hkv, max_blocks] (int32 page ids)."""
@@ -86,6 +92,55 @@ def kv_cache(K: torch.Tensor, V: torch.Tensor | None = None,
         c.block_table = block_table.data_ptr()
         c.max_blocks = block_table.shape[1]
     return c
+
+
+def kv_batch(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor | None = None) -> KvCache:
+    """A zha_kv_cache over the caches of a batch: contiguous K, V [n_seqs, Hkv, ld, d]
+    when block_table is None, else page pools [n_pages, C, d] and block_table
+    [n_seqs, Hkv, max_blocks] int32. It keeps the tensors alive."""
+    for x in (K, V):
+        if not (x.is_cuda and x.is_contiguous() and x.dim() == (4 if block_table is None else 3)):
+            raise ValueError("caches must be contiguous CUDA tensors [n_seqs, Hkv, ld, d], or pools [n_pages, C, d]")
+    if K.shape != V.shape or K.dtype != V.dtype or K.device != V.device:
+        raise ValueError("K and V must have one shape, type and device")
+    c = KvCache()
+    c.k, c.v = K.data_ptr(), V.data_ptr()
+    c.ld = K.shape[2] if block_table is None else K.shape[0]
+    if block_table is not None:
+        if not (block_table.device == K.device and block_table.dtype == torch.int32
+                and block_table.is_contiguous() and block_table.dim() == 3):
+            raise ValueError("block_table must be a contiguous int32 CUDA tensor [n_seqs, Hkv, max_blocks]")
+        c.block_table = block_table.data_ptr()
+        c.max_blocks = block_table.shape[2]
+    # what the calls check a configuration against (not part of the C struct)
+    c.tensors = (K, V, block_table)
+    c.shape = tuple(K.shape)
+    c.dtype = _DTYPE[K.dtype]
+    c.seqs = K.shape[0] if block_table is None else block_table.shape[0]
+    c.heads = K.shape[1] if block_table is None else block_table.shape[1]
+    c.device = K.device
+    return c
+
+
+class Rows(ctypes.Structure):
+    """zha_rows: rows of one head each, with token and head strides in elements."""
+    _fields_ = [("data", c_void_p), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("pairs", c_int32), ("layout", c_int32), ("scaling", c_int32),
+                ("freq_dim", c_int32), ("reserved", c_int32), ("base", c_double), ("factor", c_double),
+                ("original_tokens", c_double), ("low", c_double), ("high", c_double), ("amplitude", c_double)]
+
+
+class RopeTable(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("pairs", c_int32), ("layout", c_int32), ("amplitude", c_float),
+                ("turn", c_uint64 * 64)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("n_pages", c_int64), ("block_table", c_void_p),
+                ("max_blocks", c_int64), ("refs", c_void_p), ("n_seqs", c_int32), ("reserved", c_int32)]
 
 
 class Config(ctypes.Structure):
@@ -131,6 +186,16 @@ def _load() -> ctypes.CDLL:
         "zha_append_chunk_kv": (c_int32, [P, POINTER(KvCache), c_int64, P]),
         "zha_sparse_attend_kv": (c_int32, [P, P, POINTER(KvCache), c_int64, c_int32, P, P, c_int32, P, P,
                                            P, c_size_t, P, P]),
+        "zha_rope_init": (c_int32, [POINTER(RopeSpec), POINTER(RopeTable)]),
+        "zha_rope_apply": (c_int32, [P, P, c_int32, P, c_int64, c_int32, c_int32, P, c_int32, P]),
+        "zha_rope_append_kv": (c_int32, [P, P, P, P, P, c_int32, c_int64, P, c_int32, P, P, P, P, c_int32, P, P]),
+        "zha_attend_batch_workspace_bytes": (c_size_t, [P, c_int32, c_int64]),
+        "zha_attend_batch_kv": (c_int32, [P, P, c_int32, P, c_int32, P, c_int64, P, P, P, c_size_t, P, P]),
+        "zha_pages_workspace_bytes": (c_size_t, [P, P, c_int32]),
+        "zha_pages_extend": (c_int32, [P, P, P, P, c_int32, P, c_size_t, P, P]),
+        "zha_pages_fork": (c_int32, [P, P, P, P, P, c_int32, P, c_size_t, P, P]),
+        "zha_pages_free": (c_int32, [P, P, P, P, c_int32, P, P]),
+        "zha_pages_compact": (c_int32, [P, P, P, P, P, c_size_t, P, P]),
         "zha_diagnostics_workspace_bytes": (c_size_t, [POINTER(Config), c_int32, c_int64]),
         "zha_route_diagnostics": (c_int32, [P, P, P, c_int64, c_int32, c_int64, P, P, P, c_size_t, P]),
         "zha_tree_debug": (c_int32, [P, ctypes.c_uint32, c_int32]),
@@ -371,3 +436,212 @@ class Tree:
                                     ptr(lse), ptr(ws), ws.numel() * ws.element_size(), ptr(status),
                                     stream_ptr(stream)), "zha_sparse_attend")
         return out, lse
+
+
+# ---- Batches of caches -------------------------------------------------------
+# The wrappers below check what the C calls cannot see (shapes, types, devices)
+# and pass pointers; checks of values are the library's. Like all calls here they
+# run on the current device's current stream unless given one.
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _args(device, status, ws=None) -> None:
+    """The current device's tensors, a status word and a workspace."""
+    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
+          "tensors must lie on the current CUDA device")
+    _need(status is None or (status.dtype == torch.int32 and status.device == device),
+          "status must be an int32 tensor on the same device")
+    _need(ws is None or (ws.device == device and ws.is_contiguous()),
+          "ws must be a contiguous tensor on the same device")
+
+
+def _int_list(x: torch.Tensor, dtype, n: int, device, name: str) -> int:
+    _need(x.dtype == dtype and x.device == device and x.shape == (n,) and x.is_contiguous(),
+          f"{name} must be a contiguous {dtype} tensor [{n}] on the same device")
+    return x.data_ptr()
+
+
+def _same_cache(cfg: Config, c) -> None:
+    """A configuration and a kv_batch() or page_pool() that describe one cache."""
+    s = c.shape
+    _need(c.heads == cfg.n_kv_heads and s[-1] == cfg.head_dim and c.dtype == cfg.kv_dtype
+          and (len(s) == 4 or s[1] == cfg.chunk), "the cache does not match the configuration")
+
+
+class Rope:
+    """A rotation (zha_rope_init): `layout` "interleaved" or "half", `scaling` "none",
+    "linear", "ntk", "yarn" or "bands". pairs None: the whole head."""
+
+    LAYOUTS = {"interleaved": 0, "half": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+    def __init__(self, head_dim: int, pairs: int | None = None, layout: str = "interleaved",
+                 base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_tokens: float = 0.0, low: float = 0.0, high: float = 0.0,
+                 freq_dim: int = 0, amplitude: float = 0.0):
+        _need(layout in self.LAYOUTS and scaling in self.SCALINGS, "unknown layout or scaling")
+        spec = RopeSpec(head_dim, head_dim // 2 if pairs is None else pairs, self.LAYOUTS[layout],
+                        self.SCALINGS[scaling], freq_dim, 0, base, factor, original_tokens, low, high, amplitude)
+        self.table = RopeTable()
+        check(lib.zha_rope_init(byref(spec), byref(self.table)), "zha_rope_init")
+
+
+def _rows(x: torch.Tensor, tokens: int, heads: int, d: int, device, name: str) -> Rows:
+    _need(x.shape == (tokens, heads, d) and x.device == device and (x.stride(2) == 1 or x.numel() == 0),
+          f"{name} must be [{tokens}, {heads}, {d}] with rows of adjacent elements, on the same device")
+    return Rows(x.data_ptr(), x.stride(0) if tokens > 1 else 0, x.stride(1) if heads > 1 else 0)
+
+
+def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | None = None,
+               inverse: bool = False, stream=None) -> torch.Tensor:
+    """zha_rope_apply: x [T, heads, d] (float32 or bf16, any token and head strides) turned
+    at pos [T] int64, or turned back (the gradient's direction). `out` may be x."""
+    _need(x.dim() == 3 and x.dtype in _DTYPE, "x must be [T, heads, d], float32 or bfloat16")
+    T, H, d = x.shape
+    _need(d == rope.table.head_dim, "x does not match the rotation's head_dim")
+    dev = x.device
+    _args(dev, None)
+    if out is None:
+        out = torch.empty(T, H, d, dtype=x.dtype, device=dev)
+    _need(out.dtype in _DTYPE, "out must be float32 or bfloat16")
+    rx, ry = _rows(x, T, H, d, dev, "x"), _rows(out, T, H, d, dev, "out")
+    check(lib.zha_rope_apply(byref(rope.table), byref(rx), _DTYPE[x.dtype], _int_list(pos, torch.int64, T, dev, "pos"),
+                             T, H, 1 if inverse else 0, byref(ry), _DTYPE[out.dtype], stream_ptr(stream)),
+          "zha_rope_apply")
+    return out
+
+
+def rope_append_kv(cfg: Config, rope: Rope | None, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                   kv: KvCache, n_seqs: int, seq: torch.Tensor, index: torch.Tensor,
+                   pos: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                   q_dtype: torch.dtype = torch.float32, status: torch.Tensor | None = None, stream=None):
+    """zha_rope_append_kv: k, v [T, Hkv, d] into the caches of kv_batch() at row index[t] of
+    sequence seq[t], keys turned at pos (None: index); q [T, Hq, d] turned into q_out, which
+    is returned (None without q). rope None: nothing is turned."""
+    _same_cache(cfg, kv)
+    _need(1 <= n_seqs <= kv.seqs, "n_seqs is more than the caches hold")
+    T, H, Hq, d = k.shape[0], cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
+    dev = kv.device
+    _args(dev, status)
+    _need(k.dtype in _DTYPE and v.dtype == k.dtype and (q is None or q.dtype == k.dtype),
+          "q, k and v must have one type, float32 or bfloat16")
+    rk, rv = _rows(k, T, H, d, dev, "k"), _rows(v, T, H, d, dev, "v")
+    rq = None
+    if q is not None:
+        rq = _rows(q, T, Hq, d, dev, "q")
+        if q_out is None:
+            q_out = torch.empty(T, Hq, d, dtype=q_dtype, device=dev)
+        _need(q_out.shape == (T, Hq, d) and q_out.is_contiguous() and q_out.device == dev and q_out.dtype in _DTYPE,
+              f"q_out must be a contiguous float32 or bfloat16 tensor [{T}, {Hq}, {d}]")
+    check(lib.zha_rope_append_kv(
+        byref(cfg), None if rope is None else byref(rope.table), None if rq is None else byref(rq), byref(rk), byref(rv),
+        _DTYPE[k.dtype], T, byref(kv), n_seqs, _int_list(seq, torch.int32, T, dev, "seq"),
+        _int_list(index, torch.int64, T, dev, "index"), None if pos is None else _int_list(pos, torch.int64, T, dev, "pos"),
+        None if q is None else q_out.data_ptr(), ZHA_F32 if q is None else _DTYPE[q_out.dtype],
+        ptr(status), stream_ptr(stream)), "zha_rope_append_kv")
+    return None if q is None else q_out
+
+
+def attend_batch_workspace_bytes(cfg: Config, n_seqs: int, max_tokens: int) -> int:
+    return int(lib.zha_attend_batch_workspace_bytes(byref(cfg), n_seqs, max_tokens))
+
+
+def attend_batch_kv(cfg: Config, Q: torch.Tensor, kv: KvCache, n_seqs: int, n_tokens: torch.Tensor, max_tokens: int,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream=None):
+    """zha_attend_batch_kv: Q [n_seqs, Hq, d] (float32 or bf16) over the first n_tokens [n_seqs]
+    (int64) tokens of each cache of kv_batch(); (out, lse), out of Q's type."""
+    _same_cache(cfg, kv)
+    _need(1 <= n_seqs <= kv.seqs, "n_seqs is more than the caches hold")
+    dev = kv.device
+    want = (n_seqs, cfg.n_q_heads, cfg.head_dim)
+    _need(Q.shape == want and Q.dtype in _DTYPE and Q.is_contiguous() and Q.device == dev,
+          f"Q must be a contiguous float32 or bfloat16 tensor {list(want)} on the cache's device")
+    if out is None:
+        out = torch.empty_like(Q)
+    if lse is None:
+        lse = torch.empty(want[:2], dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = _bytes_tensor(attend_batch_workspace_bytes(cfg, n_seqs, max_tokens), dev)
+    _args(dev, status, ws)
+    _need(out.shape == want and out.dtype == Q.dtype and out.is_contiguous() and out.device == dev,
+          "out must be a contiguous tensor of Q's shape and type")
+    _need(lse.shape == want[:2] and lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev,
+          "lse must be a contiguous float32 tensor [n_seqs, Hq]")
+    check(lib.zha_attend_batch_kv(byref(cfg), Q.data_ptr(), _DTYPE[Q.dtype], byref(kv), n_seqs,
+                                  _int_list(n_tokens, torch.int64, n_seqs, dev, "n_tokens"), max_tokens,
+                                  out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  ptr(status), stream_ptr(stream)), "zha_attend_batch_kv")
+    return out, lse
+
+
+def page_pool(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor, refs: torch.Tensor) -> PagePool:
+    """A zha_page_pool over K, V [n_pages, C, d], block_table [n_seqs, Hkv, max_blocks] and refs
+    [n_pages] (both int32). It keeps the tensors alive."""
+    kv = kv_batch(K, V, block_table)
+    _int_list(refs, torch.int32, K.shape[0], K.device, "refs")
+    p = PagePool(kv.k, kv.v, kv.ld, kv.block_table, kv.max_blocks, refs.data_ptr(), block_table.shape[0], 0)
+    p.tensors = (*kv.tensors, refs)
+    p.shape, p.dtype, p.heads, p.seqs, p.device = kv.shape, kv.dtype, kv.heads, kv.seqs, kv.device
+    return p
+
+
+def pages_workspace_bytes(cfg: Config, pool: PagePool, n_items: int) -> int:
+    return int(lib.zha_pages_workspace_bytes(byref(cfg), byref(pool), n_items))
+
+
+def _pages(cfg, pool, n_items, ws, status, need_ws=True):
+    _same_cache(cfg, pool)
+    if ws is None and need_ws:
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n_items), pool.device)
+    _args(pool.device, status, ws)
+    return ws
+
+
+def pages_extend(cfg: Config, pool: PagePool, seqs: torch.Tensor, n_tokens: torch.Tensor,
+                 ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """zha_pages_extend: pages for the first n_tokens[i] (int64) tokens of sequence seqs[i] (int32)."""
+    n = seqs.numel()
+    ws = _pages(cfg, pool, n, ws, status)
+    check(lib.zha_pages_extend(byref(cfg), byref(pool), _int_list(seqs, torch.int32, n, pool.device, "seqs"),
+                               _int_list(n_tokens, torch.int64, n, pool.device, "n_tokens"), n, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), ptr(status), stream_ptr(stream)), "zha_pages_extend")
+
+
+def pages_fork(cfg: Config, pool: PagePool, src: torch.Tensor, dst: torch.Tensor, n_tokens: torch.Tensor,
+               ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """zha_pages_fork: the empty sequence dst[i] becomes the first n_tokens[i] tokens of src[i]."""
+    n = dst.numel()
+    ws = _pages(cfg, pool, n, ws, status)
+    dev = pool.device
+    check(lib.zha_pages_fork(byref(cfg), byref(pool), _int_list(src, torch.int32, n, dev, "src"),
+                             _int_list(dst, torch.int32, n, dev, "dst"),
+                             _int_list(n_tokens, torch.int64, n, dev, "n_tokens"), n, ws.data_ptr(),
+                             ws.numel() * ws.element_size(), ptr(status), stream_ptr(stream)), "zha_pages_fork")
+
+
+def pages_free(cfg: Config, pool: PagePool, seqs: torch.Tensor, keep: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """zha_pages_free: sequences seqs [n] give up their pages behind the first keep [n] (int64)
+    tokens (None: all). Needs no workspace; ws is taken for symmetry and not used."""
+    n = seqs.numel()
+    _pages(cfg, pool, n, ws, status, need_ws=False)
+    check(lib.zha_pages_free(byref(cfg), byref(pool), _int_list(seqs, torch.int32, n, pool.device, "seqs"),
+                             None if keep is None else _int_list(keep, torch.int64, n, pool.device, "keep"), n,
+                             ptr(status), stream_ptr(stream)), "zha_pages_free")
+
+
+def pages_compact(cfg: Config, pool: PagePool, page_map: torch.Tensor | None = None, n_live: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """zha_pages_compact: the pages in use become [0, n); page_map [n_pages] and n_live [1]
+    (int32, both may be None) say where each went and how many they are."""
+    ws = _pages(cfg, pool, 0, ws, status)
+    dev = pool.device
+    check(lib.zha_pages_compact(
+        byref(cfg), byref(pool),
+        None if page_map is None else _int_list(page_map, torch.int32, pool.shape[0], dev, "page_map"),
+        None if n_live is None else _int_list(n_live, torch.int32, 1, dev, "n_live"), ws.data_ptr(),
+        ws.numel() * ws.element_size(), ptr(status), stream_ptr(stream)), "zha_pages_compact")

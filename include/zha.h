@@ -61,6 +61,9 @@ typedef enum {
 #define ZHA_DEV_BAD_SELECTION 2       /* zha_sparse_attend: a chunk list had an id out of range, was not strictly ascending, or a count outside [0, max_sel]; out-of-range ids are never read, and which in-range entries of such a list are attended is unspecified */
 #define ZHA_DEV_TIMEOUT 4             /* a kernel's bounded wait for its tensor-core work ran out; its outputs are not valid (it released its resources and returned) */
 #define ZHA_DEV_BAD_PAGE 8            /* a paged cache's block table named a page outside the pool (or lacked an entry); those keys were not read (treated as absent) and the outputs that needed them are not valid */
+#define ZHA_DEV_BAD_LENGTH 16         /* a token count in device memory was outside its range: clamped (zha_attend_batch_kv), or its list item refused (zha_pages_*) */
+#define ZHA_DEV_NO_PAGES 32           /* zha_pages_extend / zha_pages_fork: fewer free pages than the call needs; the call changed nothing */
+#define ZHA_DEV_BAD_SEQUENCE 64       /* a sequence index out of range, listed twice, or in conflict with another item of its list: that item was refused */
 
 typedef enum { ZHA_F32 = 0, ZHA_BF16 = 1 } zha_dtype;
 
@@ -310,6 +313,188 @@ zha_status zha_sparse_attend_kv(const zha_tree* tree, const float* d_Q, const zh
                                 int64_t n_tokens, int32_t batch, const int32_t* d_chunk_ids,
                                 const int32_t* d_n_chunks, int32_t max_sel, float* d_O, float* d_lse,
                                 void* d_ws, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* ---- A batch of caches ---------------------------------------------------------
+ * The calls below serve n_seqs sequences at once. Their zha_kv_cache holds the
+ * caches one behind the other: contiguous [n_seqs][n_kv_heads][ld][head_dim], or
+ * paged with a block table [n_seqs][n_kv_heads][max_blocks] over one pool of pages
+ * (entries < 0: no page). Sequence s alone is the cache at table row s (or at
+ * element s * n_kv_heads * ld * head_dim), as the tree's calls take it. Of the
+ * zha_config they read the head counts, head_dim, chunk and kv_dtype; rope_pairs
+ * and the tree's own fields must be valid but play no part. At most 2^31 - 512 token
+ * slots per pool and 65535 sequences. */
+
+/* ---- Rotary positions [Attention: "Attention 은 순서를 모르므로 위치 정보를 따로
+ * 넣는다"] ------------------------------------------------------------------------
+ * Pair i of a head is turned by pos * theta_i: (a, b) -> A (a cos - b sin, a sin +
+ * b cos), with theta_i = base^(-2i / freq_dim). The elements behind the pairs
+ * stay as they are. Angles are kept as 64-bit fractions of a turn, so that a
+ * far position loses nothing. */
+typedef enum {
+    ZHA_ROPE_INTERLEAVED = 0, /* pair i = elements (2i, 2i + 1), the tree's layout (rope_pairs) */
+    ZHA_ROPE_HALF = 1         /* pair i = elements (i, i + pairs) */
+} zha_rope_layout;
+
+typedef enum {
+    ZHA_ROPE_PLAIN = 0,
+    ZHA_ROPE_LINEAR = 1, /* theta_i / factor: positions interpolated */
+    ZHA_ROPE_NTK = 2,    /* base * factor^(freq_dim / (freq_dim - 2)); freq_dim 2: as LINEAR */
+    ZHA_ROPE_YARN = 3,   /* theta_i (1 - w) + theta_i / factor * w, w = clamp((i - lo) / max(hi - lo, 0.001)) to
+                            [0, 1], lo = max(0, floor(x(high))), hi = min(pairs - 1, ceil(x(low))), x(n) = freq_dim
+                            ln(original_tokens / (2 pi n)) / (2 ln base): the pairs that turn more than `high`
+                            times over the original length stay, those below `low` turns are
+                            interpolated. amplitude 0 stands for 0.1 ln(factor) + 1 */
+    ZHA_ROPE_BANDS = 4   /* by turns n = original_tokens theta_i / (2 pi): n >= high stays, n <= low is divided
+                            by factor, between them w theta_i + (1 - w) theta_i / factor, w = (n - low) /
+                            (high - low) */
+} zha_rope_scaling;
+
+typedef struct {
+    int32_t head_dim;        /* 64 or 128 */
+    int32_t pairs;           /* 1..head_dim/2 turned pairs */
+    int32_t layout;          /* zha_rope_layout */
+    int32_t scaling;         /* zha_rope_scaling */
+    int32_t freq_dim;        /* the exponent's divisor; 0: 2 * pairs (zha_config's rope_pairs uses head_dim) */
+    int32_t reserved;        /* must be 0 */
+    double base;             /* > 1 */
+    double factor;           /* >= 1, read unless PLAIN */
+    double original_tokens;  /* > 0, read by YARN and BANDS */
+    double low, high;        /* 0 < low < high, read by YARN and BANDS */
+    double amplitude;        /* A, >= 0; 0: 1 (YARN: 0.1 ln(factor) + 1) */
+} zha_rope_spec;
+
+/* A rotation ready for use: plain host data, filled by zha_rope_init. */
+typedef struct {
+    int32_t head_dim, pairs, layout;
+    float amplitude;
+    uint64_t turn[64]; /* theta_i / (2 pi) as a fraction of 2^64 */
+} zha_rope;
+
+zha_status zha_rope_init(const zha_rope_spec* spec, zha_rope* out);
+
+/* Rows of one head each: element e of head h of token t at data + t * token_stride
+ * + h * head_stride + e (strides in elements, rows 16-byte aligned). */
+typedef struct {
+    const void* data;
+    int64_t token_stride, head_stride;
+} zha_rows;
+
+/* Turn n_heads rows of each of n_tokens tokens at positions d_pos [n_tokens]
+ * (int64, any sign). inverse != 0 turns back by the same angles and multiplies
+ * by the same amplitude: the transpose, which is the gradient's map from y to x.
+ * y (y->data is written) may be x itself with the same type and strides, and must not
+ * overlap x otherwise; its rows must lie apart, which is judged by the strides (the
+ * smaller spans a row, the larger all rows of the other kind). Types are zha_dtype
+ * values; the arithmetic is float32. n_tokens = 0
+ * does nothing. */
+zha_status zha_rope_apply(const zha_rope* rope, const zha_rows* x, int32_t x_dtype,
+                          const int64_t* d_pos, int64_t n_tokens, int32_t n_heads, int32_t inverse,
+                          const zha_rows* y, int32_t y_dtype, void* stream);
+
+/* The new tokens of a batch into its caches: for each of n_new tokens t, key and
+ * value rows k, v (n_kv_heads each, element type src_dtype) go to cache row
+ * d_index[t] of sequence d_seq[t] in kv_dtype, the keys turned at position
+ * d_pos[t] (NULL: d_index), and the query rows q (n_q_heads; NULL: none),
+ * turned the same way, to d_q_out [n_new][n_q_heads][head_dim] of type q_dtype,
+ * as zha_route, zha_sparse_attend (float32) and zha_attend_batch_kv take them. rope
+ * NULL: position-free keys, nothing is turned. kv->k and kv->v are written.
+ *  - d_seq[t] < 0: padding; nothing of that token is read or written.
+ *  - d_seq[t] >= n_seqs, or d_index[t] outside the table or ld: nothing of that token
+ *    is written, ZHA_DEV_BAD_SEQUENCE. A table entry outside the pool: that
+ *    head's key and value are not written, ZHA_DEV_BAD_PAGE.
+ *  - Two tokens with the same sequence and index, or whose sequences share that
+ *    page, leave either's values there (per element); zha_pages_fork keeps
+ *    part-filled pages apart for this reason.
+ * d_q_out must not overlap the inputs. n_new = 0 does nothing. */
+zha_status zha_rope_append_kv(const zha_config* cfg, const zha_rope* rope, const zha_rows* q,
+                              const zha_rows* k, const zha_rows* v, int32_t src_dtype, int64_t n_new,
+                              const zha_kv_cache* kv, int32_t n_seqs, const int32_t* d_seq,
+                              const int64_t* d_index, const int64_t* d_pos, void* d_q_out,
+                              int32_t q_dtype, int32_t* d_status, void* stream);
+
+/* ---- Dense attention of a batch [Attention: "FlashAttention 계열"] -----------------
+ * One query token per sequence over all of its keys: o = sum_{j < n} softmax_j(q.k_j /
+ * sqrt(d)) v_j with n = d_n_tokens[s] (int64, in device memory), query head h on KV head
+ * h / (n_q_heads / n_kv_heads). The dense arm of the decode step, for short
+ * contexts, which routing does not pay for, and to measure routing against. d_Q and
+ * d_O [n_seqs][n_q_heads][head_dim] have type q_dtype (float32 or bf16), d_lse
+ * (nullable) float32 [n_seqs][n_q_heads]. n = 0, or no page of the sequence
+ * in the pool: o = 0, lse = -inf. A count outside [0, max_tokens] is clamped
+ * (ZHA_DEV_BAD_LENGTH). Keys whose table entry is outside the pool count as
+ * absent (ZHA_DEV_BAD_PAGE). Rows behind n are not read. Requires max_tokens <= ld, or
+ * <= max_blocks * C. The split over the cache is made on the device from the counts,
+ * so a captured call may be replayed with other counts. The workspace holds
+ * nothing between calls; calls that may overlap need one each. A float32 result
+ * is exact to float32 rounding for finite inputs (a bf16 cache's keys and values enter
+ * exactly, queries and weights as three bf16 terms or two tf32 terms); with bf16
+ * queries, weights are two bf16 terms. An infinity or NaN among the inputs makes the
+ * results of its own head and sequence infinite or NaN, no others. */
+size_t zha_attend_batch_workspace_bytes(const zha_config* cfg, int32_t n_seqs, int64_t max_tokens);
+zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q_dtype,
+                               const zha_kv_cache* kv, int32_t n_seqs, const int64_t* d_n_tokens,
+                               int64_t max_tokens, void* d_O, float* d_lse, void* d_ws,
+                               size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* ---- Pages of a batch [Attention: "KV cache 를 담는 방식을 바꾼다: PagedAttention,
+ * 양자화"] ------------------------------------------------------------------------
+ * Which pages are in use is the pool's reference counts, in device memory: refs[p] =
+ * the table entries that name page p, 0 = free. The calls run on the device alone
+ * (capturable) and always hand out the lowest free pages, in the order item, KV head,
+ * block, so that a run can be repeated exactly. Lists are int32 [n_items] sequence
+ * indexes with int64 token counts. An item whose index is out of range or
+ * already listed is refused (ZHA_DEV_BAD_SEQUENCE), one whose count does not fit in
+ * max_blocks pages too (ZHA_DEV_BAD_LENGTH); the others go ahead. n_items = 0 does
+ * nothing. Calls on one pool need an order (a stream) between them. */
+typedef struct {
+    void* k;                /* K pool [n_pages][C][head_dim] */
+    void* v;                /* V pool, the same shape */
+    int64_t n_pages;
+    int32_t* block_table;   /* [n_seqs][n_kv_heads][max_blocks], < 0: no page */
+    int64_t max_blocks;
+    int32_t* refs;          /* [n_pages] */
+    int32_t n_seqs;
+    int32_t reserved;       /* must be 0 */
+} zha_page_pool;
+
+/* Workspace of zha_pages_extend, _fork (n_items) and _compact (n_items = 0); holds
+ * nothing between calls. */
+size_t zha_pages_workspace_bytes(const zha_config* cfg, const zha_page_pool* pool, int32_t n_items);
+
+/* A page for every block without one among the first ceil(d_n_tokens[i] / C) blocks of
+ * each KV head of sequence d_seqs[i]. All items or, when the free pages do
+ * not suffice, none (ZHA_DEV_NO_PAGES). */
+zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_seqs,
+                            const int64_t* d_n_tokens, int32_t n_items, void* d_ws, size_t ws_bytes,
+                            int32_t* d_status, void* stream);
+
+/* Sequence d_dst[i] becomes a copy of the first d_n_tokens[i] tokens of d_src[i]:
+ * full pages are shared (refs + 1), the rows in use of a part-filled last page are
+ * copied to a page of its own, whose other rows stay as they were. One source may
+ * serve many items. A destination must be empty (all entries < 0), no source may be
+ * a destination of the same list, and the source's blocks must be pages in use
+ * (else ZHA_DEV_BAD_PAGE); such an item is refused. All items that are not refused or,
+ * without enough free pages, none (ZHA_DEV_NO_PAGES). */
+zha_status zha_pages_fork(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_src,
+                          const int32_t* d_dst, const int64_t* d_n_tokens, int32_t n_items, void* d_ws,
+                          size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* Give up the blocks from ceil(d_keep[i] / C) on (d_keep NULL: all blocks) of
+ * sequence d_seqs[i]: refs - 1, entry -1; a page at 0 is free. A sequence listed twice
+ * keeps the smaller count. An entry that names no page in use is cleared
+ * (ZHA_DEV_BAD_PAGE). Cut back inside a shared page, a sequence must not be
+ * written there: fork it first. */
+zha_status zha_pages_free(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_seqs,
+                          const int64_t* d_keep, int32_t n_items, int32_t* d_status, void* stream);
+
+/* Pack the pool: with n pages in use, the k-th of them at or above n moves
+ * (contents, count, table entries of all sequences) to the k-th free page below n,
+ * so that pages [0, n) are the ones in use. d_page_map (nullable) int32 [n_pages]:
+ * the new place of each page that was in use, -1 of a free one; d_n_live
+ * (nullable) int32: n. A table entry that names a free page becomes -1
+ * (ZHA_DEV_BAD_PAGE); one outside the pool stays. */
+zha_status zha_pages_compact(const zha_config* cfg, const zha_page_pool* pool, int32_t* d_page_map,
+                             int32_t* d_n_live, void* d_ws, size_t ws_bytes, int32_t* d_status,
+                             void* stream);
 
 /* ---- Routing diagnostics [ZHA: 어떻게 쓰나; 전제와 한계] -----------------------
  * How well each level's estimate follows the dense attention mass, for

@@ -1,0 +1,828 @@
+"""The batch calls on the GPU: rotary positions, the cache write, dense attention of
+one token per sequence and the page bookkeeping, against plain implementations in
+64 bits (attention, rotation) or in Python (pages, exact)."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def zha():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from hierarchical_sparse_attention_zha_b200 import zha as z
+    return z
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _cfg(zha, H, G, d, C, dt):
+    return zha.make_config(H, H * G, d, C, 1, 1, dt, 1 << 30)
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+class Batch:
+    """Ragged caches. Everything no sequence owns (other pages, rows behind its
+    length) is NaN, so that reading it shows."""
+
+    def __init__(self, zha, lens, H, G, d, C, cache, q, paged=True, seed=0, scale=1.0):
+        g = _gen(seed)
+        S, most = len(lens), max(max(lens), 1)
+        self.zha, self.S, self.H, self.G, self.d, self.C, self.most = zha, S, H, G, d, C, most
+        blocks = -(-most // C) + 1
+        self.cfg = _cfg(zha, H, G, d, C, cache)
+        if paged:
+            pages = S * H * blocks + 3
+            self.K = torch.full((pages, C, d), math.nan, dtype=cache, device="cuda")
+            self.V = self.K.clone()
+            perm = torch.randperm(pages, device="cuda", generator=g)
+            self.table = perm[: S * H * blocks].to(torch.int32).reshape(S, H, blocks)
+        else:
+            self.K = torch.full((S, H, most + 5, d), math.nan, dtype=cache, device="cuda")
+            self.V = self.K.clone()
+            self.table = None
+        self.n = torch.tensor(lens, dtype=torch.int64, device="cuda")
+        for s, n in enumerate(lens):
+            for h in range(H):
+                for x in (self.K, self.V):
+                    x[self.rows(s, h, n)] = (torch.randn(n, d, device="cuda", generator=g) * scale).to(cache)
+        if paged:       # entries behind the length name nothing
+            for s, n in enumerate(lens):
+                self.table[s, :, -(-n // C):] = -1
+        self.kv = zha.kv_batch(self.K, self.V, self.table)
+        self.Q = (torch.randn(S, H * G, d, device="cuda", generator=g) * 2).to(q)
+
+    def rows(self, s, h, n):
+        if self.table is None:
+            return s, h, slice(0, n)
+        t = torch.arange(n, device="cuda")
+        return self.table[s, h].long()[t // self.C], t % self.C
+
+    def run(self, **kw):
+        return self.zha.attend_batch_kv(self.cfg, self.Q, self.kv, self.S, self.n, kw.pop("max_tokens", self.most), **kw)
+
+    def check(self, out, lse, absent=lambda s, h, n: None):
+        """Against the 64-bit definition. A score is the sum of d exact products: at most
+        d/8 + 8 additions of matrix instructions or lanes, each off by 2^-23 of the sum
+        of magnitudes, and one scaling. A weight exp(x - m) is then off by twice that
+        (x and m) and 2^-21, weights enter with 2^-16 (bf16 queries: two bf16 terms) or
+        2^-22, and an output is a sum over n keys, at most n/8 + 300 additions."""
+        o64 = torch.zeros(self.S, self.H * self.G, self.d, dtype=torch.float64, device="cuda")
+        l64 = torch.full(o64.shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+        to, tl = torch.zeros_like(l64), torch.zeros_like(l64)
+        q16 = self.Q.dtype == BF
+        for s, n in enumerate(self.n.clamp(0, self.most).tolist()):
+            for h in range(self.H if n else 0):
+                K, V = (x[self.rows(s, h, n)].double() for x in (self.K, self.V))
+                keep = absent(s, h, n)
+                if keep is not None:
+                    K, V = K[keep], V[keep]
+                if len(K) == 0:
+                    continue
+                heads = slice(h * self.G, (h + 1) * self.G)
+                q = self.Q[s, heads].double()
+                w = q @ K.T / math.sqrt(self.d)
+                l64[s, heads] = torch.logsumexp(w, 1)
+                o64[s, heads] = torch.softmax(w, 1) @ V
+                ex = (self.d / 8 + 9) * 2.0 ** -23 * (q.abs() @ K.abs().T).amax(1) / math.sqrt(self.d)
+                eo = 2 * (2 * ex + 2.0 ** -21 + (2.0 ** -16 if q16 else 2.0 ** -22))
+                to[s, heads] = (eo + (len(K) / 8 + 300) * 2.0 ** -23) * V.abs().amax()
+                tl[s, heads] = ex + 2.0 ** -20 + 2.0 ** -22 * l64[s, heads].abs()
+        tol = to[..., None] + (2.0 ** -8 if q16 else 0.0) * o64.abs()
+        assert ((out.double() - o64).abs() <= tol).all(), ((out.double() - o64).abs() / tol.clamp(min=1e-30)).max()
+        seen = torch.isfinite(l64)
+        assert (seen == torch.isfinite(lse)).all() and (lse[~seen] == -math.inf).all()
+        assert ((lse.double() - l64).abs()[seen] <= tl[seen]).all()
+
+
+@pytest.mark.parametrize("cache", [BF, F32])
+@pytest.mark.parametrize("q", [BF, F32])
+@pytest.mark.parametrize("d,H,G,C,paged", [(128, 2, 8, 64, True), (64, 1, 4, 16, True), (128, 3, 1, 7, True),
+                                           (64, 2, 5, 128, False), (128, 1, 12, 2, True), (64, 1, 16, 33, True),
+                                           (128, 2, 3, 64, False), (64, 1, 33, 16, True), (128, 1, 16, 64, True)])
+def test_attend_matches_the_definition(zha, cache, q, d, H, G, C, paged):
+    b = Batch(zha, [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 300, 1025, 0], H, G, d, C, cache, q, paged, seed=d + G)
+    st = _status()
+    out, lse = b.run(status=st)
+    b.check(out, lse)
+    assert int(st) == 0
+    out2, lse2 = b.run()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("cache,q,G,n", [(BF, F32, 8, 200003), (F32, F32, 4, 50001), (BF, BF, 16, 100000),
+                                         (BF, BF, 4, 33333)])
+def test_attend_splits_long_sequences(zha, cache, q, G, n):
+    """Units cut over many blocks, beside short and empty ones."""
+    b = Batch(zha, [n, 0, 5, n // 3, 1], 1, G, 128, 64, cache, q, seed=3)
+    b.check(*b.run())
+
+
+def test_attend_many_short_sequences(zha):
+    lens = [(i * 37) % 200 for i in range(700)]
+    b = Batch(zha, lens, 2, 2, 64, 16, BF, F32, seed=4)
+    b.check(*b.run())
+    b.check(*b.run(max_tokens=b.most))
+
+
+def test_attend_keeps_the_low_bits_of_queries_and_weights(zha):
+    """Low bits that all point the same way: a dropped third term of the queries
+    would be off by about 2^-17 of the score, beyond the bound of check()."""
+    for cache in (BF, F32):
+        b = Batch(zha, [16, 1], 1, 4, 128, 16, cache, F32, seed=5)
+        b.Q[:] = 1.0 + 2.0 ** -8 + 2.0 ** -16 + 2.0 ** -17
+        b.K[:] = b.K.abs()
+        b.kv = zha.kv_batch(b.K, b.V, b.table)
+        b.check(*b.run())
+
+
+def test_attend_large_scores_and_equal_scores(zha):
+    b = Batch(zha, [300, 77], 1, 8, 64, 16, BF, F32, seed=6, scale=30.0)
+    b.check(*b.run())
+    b.Q.zero_()                                   # every weight 1: the mean of V
+    b.check(*b.run())
+
+
+def test_attend_values_that_are_not_finite_stay_in_their_head(zha):
+    b = Batch(zha, [40, 40, 40], 2, 2, 64, 16, F32, F32, paged=False, seed=7)
+    want, wlse = b.run()
+    b.K[0, 0, 3] = -math.inf
+    b.K[1, 0, :40] = math.nan
+    b.V[2, 1, 39, 5] = math.inf
+    out, lse = b.run()
+    assert torch.equal(out[:2, 2:], want[:2, 2:]) and torch.equal(lse[:2, 2:], wlse[:2, 2:])
+    assert torch.equal(out[2, :2], want[2, :2]) and torch.equal(lse[2], wlse[2])
+    assert out[1, :2].isnan().all() and lse[1, :2].isnan().all()
+    assert not torch.isfinite(out[2, 2:, 5]).any()
+
+
+def test_attend_bad_lengths_are_clamped(zha):
+    b = Batch(zha, [50, 60, 70], 2, 4, 64, 16, BF, F32, seed=8)
+    for lens in ([50, -3, 70], [50, 60, 1 << 40]):
+        b.n = torch.tensor(lens, dtype=torch.int64, device="cuda")
+        st = _status()
+        out, lse = b.run(status=st)
+        b.check(out, lse)
+        assert int(st) == zha.ZHA_DEV_BAD_LENGTH
+        b.run()                                   # no status word to write
+
+
+def test_attend_bad_pages_count_as_absent(zha):
+    b = Batch(zha, [64, 100, 130], 2, 4, 64, 16, BF, F32, seed=9)
+    for s, h, blk, e in ((0, 0, 1, -1), (1, 1, 0, -(1 << 31)), (1, 1, 6, b.K.shape[0]), (2, 0, 3, (1 << 31) - 1)):
+        b.table[s, h, blk] = e
+    b.table[0, 1] = -1                            # no page at all
+    good = b.table.clone().clamp(0, b.K.shape[0] - 1)
+    bad = (b.table < 0) | (b.table >= b.K.shape[0])
+    st = _status()
+    out, lse = b.run(status=st)
+    b.table = good
+    b.check(out, lse, absent=lambda s, h, n: ~bad[s, h][torch.arange(n, device="cuda") // 16])
+    assert int(st) == zha.ZHA_DEV_BAD_PAGE
+    assert (out[0, 4:] == 0).all() and (lse[0, 4:] == -math.inf).all()
+
+
+def test_attend_some_sequences_of_a_larger_cache_and_no_tokens(zha):
+    b = Batch(zha, [10, 20, 30], 1, 4, 64, 16, BF, F32, seed=10)
+    whole, lse = b.run()
+    one, lse1 = zha.attend_batch_kv(b.cfg, b.Q[:1], b.kv, 1, b.n[:1], 10)
+    assert torch.equal(one, whole[:1]) and torch.equal(lse1, lse[:1])
+    out, lse = zha.attend_batch_kv(b.cfg, b.Q, b.kv, 3, b.n * 0, 0)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q, b.kv, 4, b.n, 30)
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q.half(), b.kv, 3, b.n, 30)
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q, b.kv, 3, b.n.int(), 30)
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(_cfg(zha, 1, 4, 64, 32, BF), b.Q, b.kv, 3, b.n, 30)
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(_cfg(zha, 1, 4, 64, 16, F32), b.Q, b.kv, 3, b.n, 30)
+
+
+def test_attend_rows_of_a_long_cache_pass_32_bit_offsets(zha):
+    """Elements beyond 2^32 bytes and 2^31 elements: 9 sequences of 4 heads of 2^19 rows
+    of 128 bf16 (4.8 GB each of K and V), the last sequence and a page at the end."""
+    S, H, ld, d = 9, 4, 1 << 19, 128
+    K = torch.zeros(S, H, ld, d, dtype=BF, device="cuda")
+    V = torch.zeros(S, H, ld, d, dtype=BF, device="cuda")
+    g = _gen(11)
+    lens = [0] * (S - 1) + [700]
+    K[8, :, :700] = torch.randn(H, 700, d, device="cuda", generator=g).to(BF)
+    V[8, :, :700] = torch.randn(H, 700, d, device="cuda", generator=g).to(BF)
+    b = Batch(zha, [0] * S, H, 2, d, 64, BF, F32, paged=False, seed=12)
+    b.K, b.V, b.most = K, V, 700
+    b.n = torch.tensor(lens, dtype=torch.int64, device="cuda")
+    b.kv = zha.kv_batch(K, V)
+    b.check(*b.run())
+    # the same memory as a pool: its last 11 pages of 64
+    pages = S * H * ld // 64
+    b.K, b.V = (x.view(pages, 64, d) for x in (K, V))
+    b.table = torch.full((S, H, 11), -1, dtype=torch.int32, device="cuda")
+    b.table[8, :] = torch.arange(pages - 11, pages, device="cuda", dtype=torch.int32)
+    b.V[pages - 11:] = torch.randn(11, 64, d, device="cuda", generator=g).to(BF)
+    b.kv = zha.kv_batch(b.K, b.V, b.table)
+    b.check(*b.run())
+
+
+def test_attend_captured_replayed_with_other_counts_and_streams(zha):
+    b = Batch(zha, [200, 3, 90], 2, 4, 128, 16, BF, F32, seed=13)
+    ws = torch.empty(zha.attend_batch_workspace_bytes(b.cfg, 3, b.most), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(b.Q)
+    lse = torch.empty(3, 8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.run(out=out, lse=lse, ws=ws)
+    side.synchronize()
+    b.check(out, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run(out=out, lse=lse, ws=ws)
+    for lens in ([200, 3, 90], [0, 0, 0], [1, 3, 17], [64, 0, 65]):
+        b.n.copy_(torch.tensor(lens))
+        ws.fill_(255)                              # nothing is kept there
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check(out, lse)
+    # another stream given by hand
+    b.run(out=out, lse=lse, ws=ws, stream=side)
+    side.synchronize()
+    b.check(out, lse)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+def _turn64(x, pos, rope_args, back=False):
+    """x [T, heads, d] in 64 bits by complex products, and the bound of the fp32
+    kernel: the angle is rounded at 2^-33 turns and, as a fraction of a half turn of at
+    most 1/4, at 2^-27; sine and cosine at 2 ulp: below 3 * 2^-24 together; two
+    products, a sum, the amplitude and its product: 5 roundings of 2^-24."""
+    a = dict(pairs=x.shape[-1] // 2, layout="interleaved", base=1e4, scaling="none", factor=1.0, amplitude=0.0)
+    a.update(rope_args)
+    P = a["pairs"]
+    D = a.get("freq_dim") or 2 * P
+    i = np.arange(P)
+    theta = a["base"] ** (-2.0 * i / D) / (a["factor"] if a["scaling"] == "linear" else 1.0)
+    amp = a["amplitude"] or 1.0
+    # positions as exact integers times theta, reduced in extended precision
+    phi = pos.cpu().numpy().astype(np.longdouble)[:, None] * theta.astype(np.longdouble)
+    phi = np.remainder(phi, 2 * np.longdouble("3.14159265358979323846264338327950288"))
+    z = (np.cos(phi) + 1j * np.sin(-phi if back else phi)).astype(np.complex128)[:, None] * amp
+    v = x.double().cpu().numpy()
+    one, two = (slice(0, P), slice(P, 2 * P)) if a["layout"] == "half" else (slice(0, 2 * P, 2), slice(1, 2 * P, 2))
+    w = z * (v[..., one] + 1j * v[..., two])
+    y, tol = v.copy(), np.zeros_like(v)
+    y[..., one], y[..., two] = w.real, w.imag
+    tol[..., one] = tol[..., two] = 8 * 2.0 ** -24 * amp * (abs(v[..., one]) + abs(v[..., two]))
+    return torch.from_numpy(y).cuda(), torch.from_numpy(tol).cuda()
+
+
+def _close(got, want, tol):
+    tol = tol + (2.0 ** -8 * (want.abs() + tol) if got.dtype == BF else 0)
+    assert ((got.double() - want).abs() <= tol).all(), ((got.double() - want).abs() - tol).max()
+
+
+@pytest.mark.parametrize("src", [BF, F32])
+@pytest.mark.parametrize("dst", [BF, F32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("d,pairs", [(128, 64), (64, 32), (128, 48), (64, 13), (128, 1), (64, 8)])
+def test_rope_apply_matches_the_formula_and_its_inverse(zha, src, dst, layout, d, pairs):
+    g = _gen(20)
+    args = dict(pairs=pairs, layout=layout, scaling="linear", factor=3.0, amplitude=1.25)
+    rope = zha.Rope(d, **args)
+    for T, H in ((1, 1), (7, 3), (130, 5)):
+        x = torch.randn(T, H, d, device="cuda", generator=g).to(src)
+        pos = torch.randint(-5000, 200000, (T,), device="cuda", generator=g)
+        pos[0] = 0
+        for back in (False, True):
+            out = torch.empty(T, H, d, dtype=dst, device="cuda")
+            assert zha.rope_apply(rope, x, pos, out=out, inverse=back) is out
+            _close(out, *_turn64(x, pos, args, back))
+
+
+def test_rope_far_positions(zha):
+    """A million, 2^31 and 2^40 tokens on, where an fp32 product of position and
+    frequency has lost the angle. The table holds theta / 2 pi < 2^-2 to 2^-54: powers of
+    the two sides that differ by two last places (2^-52 of it), a division, the cut."""
+    rope = zha.Rope(128)
+    x = torch.randn(4, 2, 128, device="cuda", generator=_gen(21))
+    for far, slack in ((1 << 20, 0.0), (1 << 31, 2 * math.pi * 2.0 ** -23), (1 << 40, 2 * math.pi * 2.0 ** -14)):
+        pos = torch.tensor([far, far + 1, -far, far - 12345], device="cuda")
+        want, tol = _turn64(x, pos, {})
+        _close(zha.rope_apply(rope, x, pos), want, tol + slack * x.abs().amax() * 2)
+
+
+def test_rope_strided_rows_in_place_and_the_rest_untouched(zha):
+    for dt, layout, pairs in ((BF, "half", 32), (F32, "interleaved", 20), (BF, "half", 21)):
+        rope = zha.Rope(64, pairs, layout)
+        args = dict(pairs=pairs, layout=layout)
+        buf = torch.randn(9, 8, 64, device="cuda", generator=_gen(22)).to(dt)
+        pos = torch.arange(9, device="cuda") * 7
+        before = buf.clone()
+        part = buf[:, 2:5]
+        want, tol = _turn64(part, pos, args)
+        assert zha.rope_apply(rope, part, pos, out=part) is part
+        _close(part, want, tol)
+        assert torch.equal(buf[:, :2], before[:, :2]) and torch.equal(buf[:, 5:], before[:, 5:])
+        # [heads, T, d] seen as [T, heads, d], read and written; every third token
+        x = before.transpose(0, 1)[:, ::3]
+        out = torch.zeros(3, 8, 64, dtype=dt, device="cuda").transpose(0, 1)
+        _close(zha.rope_apply(rope, x, pos[:8].contiguous(), out=out), *_turn64(x, pos[:8], args))
+        # one row for all tokens and heads
+        wide = before[:1, :1].expand(4, 3, 64)
+        _close(zha.rope_apply(rope, wide, pos[:4].contiguous()), *_turn64(wide, pos[:4], args))
+    assert zha.rope_apply(rope, before[:0], pos[:0]).shape == (0, 8, 64)
+    with pytest.raises(zha.ZhaError):
+        zha.rope_apply(rope, before, pos, out=before[:1].expand(9, 8, 64))
+    with pytest.raises(ValueError):
+        zha.rope_apply(rope, before, pos[:5])
+    with pytest.raises(ValueError):
+        zha.rope_apply(rope, before, pos.int())
+
+
+def test_rope_inverse_is_the_gradient(zha):
+    """<dy, R x> = <R^T dy, x>, and a central difference of the forward call: linear, so
+    exact up to the rounding of both sides."""
+    rope = zha.Rope(64, 20, "interleaved", amplitude=1.5)
+    g = _gen(23)
+    x, dy, step = (torch.randn(5, 3, 64, device="cuda", generator=g) for _ in range(3))
+    pos = torch.tensor([0, 1, 77, 5000, 123456], device="cuda")
+    dx = zha.rope_apply(rope, dy, pos, inverse=True).double()
+    up, down = (zha.rope_apply(rope, x + e * step, pos).double() for e in (0.5, -0.5))
+    lhs, rhs = (dx * step.double()).sum(), (dy.double() * (up - down)).sum()
+    size = (dy.abs().sum(-1) * (x.abs() + step.abs()).amax(-1)).double().sum()
+    assert abs(lhs - rhs) <= 3 * 16 * 2.0 ** -24 * 1.5 * size
+
+
+def test_rope_turns_as_the_tree_reads_positions(zha):
+    """freq_dim = head_dim is the tree's rope_pairs convention: a tree built on keys turned
+    by rope_apply routes like the oracle's position-aware tree would; here the
+    level-1 summary of a chunk of equal keys, de-rotated by the build, is that key."""
+    H, d, C, P = 1, 64, 16, 8
+    cfg = zha.make_config(H, 4, d, C, 1, 4, F32, 64, rope_pairs=P)
+    g = _gen(24)
+    key = torch.randn(1, 1, d, device="cuda", generator=g)
+    rope = zha.Rope(d, P, "interleaved", freq_dim=d)
+    K = zha.rope_apply(rope, key.expand(64, 1, d), torch.arange(64, device="cuda")).transpose(0, 1).contiguous()
+    tree = zha.Tree(cfg, torch.randn(1, 4, d, device="cuda", generator=g))
+    tree.build(K, 64)
+    khat, _ = tree.level(1)
+    # the tree keeps keys relative to its nodes: the unturned part must come back
+    assert (khat[..., 2 * P:] - key[..., 2 * P:]).abs().max() <= 1e-4 * key.abs().max()
+
+
+# ---------------------------------------------------------------------------
+# The cache write
+# ---------------------------------------------------------------------------
+def _append_case(zha, src, cache, q, layout, pairs, d, H, G, C, T, S, paged, seed, rope=True):
+    g = _gen(seed)
+    Hq = H * G
+    qkv = torch.randn(T, Hq + 2 * H, d, device="cuda", generator=g).to(src)
+    Q, K, V = qkv[:, :Hq], qkv[:, Hq:Hq + H], qkv[:, Hq + H:]
+    blocks = 2 + -(-T // C)
+    if paged:
+        pages = S * H * blocks + 2
+        table = torch.randperm(pages, device="cuda", generator=g)[: S * H * blocks].to(torch.int32).reshape(S, H, blocks)
+        kc = torch.full((pages, C, d), 7.0, dtype=cache, device="cuda")
+    else:
+        table, kc = None, torch.full((S, H, blocks * C, d), 7.0, dtype=cache, device="cuda")
+    vc = kc.clone()
+    args = dict(pairs=pairs, layout=layout)
+    seq = (torch.randperm(T, device="cuda", generator=g) % S).to(torch.int32)
+    index = torch.arange(T, device="cuda") + 1
+    return dict(zha=zha, cfg=_cfg(zha, H, G, d, C, cache), rope=zha.Rope(d, **args) if rope else None, args=args, Q=Q, K=K,
+                V=V, kc=kc, vc=vc, table=table, kv=zha.kv_batch(kc, vc, table), S=S, seq=seq, index=index, H=H, C=C,
+                qd=q)
+
+
+def _append_run(c, pos=None, **kw):
+    return c["zha"].rope_append_kv(c["cfg"], c["rope"], c["Q"], c["K"], c["V"], c["kv"], c["S"], c["seq"], c["index"],
+                                   pos, q_dtype=c["qd"], **kw)
+
+
+def _append_check(c, out, pos, drop=()):
+    """Every written row, and every other row still 7."""
+    plain = lambda x: (x.double(), torch.zeros_like(x, dtype=torch.float64))
+    kw, kt = _turn64(c["K"], pos, c["args"]) if c["rope"] else plain(c["K"])
+    qw, qt = _turn64(c["Q"], pos, c["args"]) if c["rope"] else plain(c["Q"])
+    live = [t for t in range(len(c["seq"])) if t not in drop]
+    if out is not None:
+        _close(out[live], qw[live], qt[live])
+    for x, w, t in ((c["kc"], kw, kt), (c["vc"], *plain(c["V"]))):
+        want = torch.full(x.shape, 7.0, dtype=torch.float64, device="cuda")
+        tol = torch.zeros_like(want)
+        for i in live:
+            s, at = int(c["seq"][i]), int(c["index"][i])
+            for h in range(c["H"]):
+                where = (s, h, at) if c["table"] is None else (int(c["table"][s, h, at // c["C"]]), at % c["C"])
+                want[where], tol[where] = w[i, h], t[i, h]
+        _close(x, want, tol)
+
+
+@pytest.mark.parametrize("src", [BF, F32])
+@pytest.mark.parametrize("cache", [BF, F32])
+@pytest.mark.parametrize("q", [BF, F32])
+@pytest.mark.parametrize("layout,pairs,d,H,G,C,T,S,paged", [
+    ("interleaved", 64, 128, 2, 4, 16, 1, 1, True), ("half", 32, 64, 1, 8, 7, 50, 3, True),
+    ("half", 13, 64, 2, 1, 64, 33, 2, False), ("interleaved", 5, 128, 4, 2, 2, 9, 5, True)])
+def test_append_writes_turned_keys_values_and_queries(zha, src, cache, q, layout, pairs, d, H, G, C, T, S, paged):
+    c = _append_case(zha, src, cache, q, layout, pairs, d, H, G, C, T, S, paged, seed=30)
+    pos = c["index"] + 99990
+    st = _status()
+    out = _append_run(c, pos, status=st)
+    assert out.dtype == q and int(st) == 0
+    _append_check(c, out, pos)
+
+
+def test_append_without_rotation_queries_or_positions(zha):
+    c = _append_case(zha, F32, F32, F32, "half", 32, 64, 2, 2, 16, 40, 2, True, seed=31)
+    out = _append_run(c)                                             # positions: the rows
+    _append_check(c, out, c["index"])
+    c = _append_case(zha, BF, BF, BF, "half", 32, 64, 2, 2, 16, 40, 2, True, seed=32, rope=False)
+    out = _append_run(c)
+    _append_check(c, out, c["index"])
+    assert torch.equal(out, c["Q"])
+    c = _append_case(zha, BF, BF, BF, "half", 32, 64, 2, 2, 16, 40, 2, True, seed=33)
+    c["Q"] = None
+    assert _append_run(c) is None
+    c["Q"] = c["K"][:, :0]
+    with pytest.raises(ValueError):
+        _append_run(c)
+
+
+def test_append_padding_and_bad_targets_write_nothing(zha):
+    c = _append_case(zha, F32, F32, F32, "interleaved", 32, 64, 2, 2, 16, 12, 2, True, seed=34)
+    c["seq"][3] = -1                                                 # padding
+    q_out = torch.full((12, 4, 64), 5.0, device="cuda")
+    st = _status()
+    out = _append_run(c, q_out=q_out, status=st)
+    assert out is q_out and int(st) == 0 and (out[3] == 5).all()
+    _append_check(c, out, c["index"], drop={3})
+    c = _append_case(zha, F32, F32, F32, "interleaved", 32, 64, 2, 2, 16, 12, 2, True, seed=34)
+    c["seq"][0], c["index"][1], c["index"][2] = 2, -1, 3 * 16        # blocks = 3
+    c["index"][4] = 1 << 40
+    q_out = torch.full((12, 4, 64), 5.0, device="cuda")
+    st = _status()
+    out = _append_run(c, q_out=q_out, status=st)
+    assert int(st) == zha.ZHA_DEV_BAD_SEQUENCE and (out[[0, 1, 2, 4]] == 5).all()
+    _append_check(c, out, c["index"], drop={0, 1, 2, 4})
+    # one head's page is missing: that head's rows are left out, queries and the other head go ahead
+    c = _append_case(zha, F32, F32, F32, "interleaved", 32, 64, 2, 2, 16, 12, 2, True, seed=35)
+    keep = c["table"].clone()
+    c["table"][1, 0] = c["kc"].shape[0]
+    c["table"][0, 0] = -1
+    st = _status()
+    out = _append_run(c, status=st)
+    assert int(st) == zha.ZHA_DEV_BAD_PAGE
+    _close(out, *_turn64(c["Q"], c["index"], c["args"]))
+    mine = keep[:, 1].flatten().long()
+    rest = torch.ones(c["kc"].shape[0], dtype=torch.bool, device="cuda")
+    rest[mine] = False
+    assert (c["kc"][rest] == 7).all() and (c["vc"][rest] == 7).all()
+    for t in range(12):
+        s, at = int(c["seq"][t]), int(c["index"][t])
+        assert torch.equal(c["vc"][keep[s, 1, at // 16].long(), at % 16], c["V"][t, 1])
+
+
+# ---------------------------------------------------------------------------
+# Pages
+# ---------------------------------------------------------------------------
+class Pages:
+    """A pool on the GPU beside a Python model of it."""
+
+    def __init__(self, zha, S, H, C, blocks, pages, d=64, dt=F32, seed=0):
+        self.zha, self.C, self.H = zha, C, H
+        self.cfg = _cfg(zha, H, 1, d, C, dt)
+        self.K = torch.randn(pages, C, d, device="cuda", generator=_gen(seed)).to(dt)
+        self.V = torch.randn(pages, C, d, device="cuda", generator=_gen(seed + 1)).to(dt)
+        self.table = torch.full((S, H, blocks), -1, dtype=torch.int32, device="cuda")
+        self.refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+        self.pool = zha.page_pool(self.K, self.V, self.table, self.refs)
+        self.k, self.v = self.K.cpu().clone(), self.V.cpu().clone()
+        self.t, self.r = self.table.cpu().numpy().copy(), self.refs.cpu().numpy().copy()
+
+    def put(self):
+        self.table.copy_(torch.from_numpy(self.t))
+        self.refs.copy_(torch.from_numpy(self.r))
+
+    def same(self):
+        assert np.array_equal(self.table.cpu().numpy(), self.t)
+        assert np.array_equal(self.refs.cpu().numpy(), self.r)
+        assert torch.equal(self.K.cpu(), self.k) and torch.equal(self.V.cpu(), self.v)
+
+    def _used(self, e):
+        return 0 <= e < len(self.r) and self.r[e] > 0
+
+    def _hand(self, need):
+        """need: (row view, block) in order; the lowest free pages, or None if too few."""
+        free = [p for p in range(len(self.r)) if self.r[p] == 0]
+        if len(need) > len(free):
+            return None
+        return free[: len(need)]
+
+    def extend(self, seqs, tokens):
+        bad, need = 0, []
+        for i, (s, n) in enumerate(zip(seqs, tokens)):
+            if not 0 <= s < len(self.t) or s in seqs[:i]:
+                bad |= self.zha.ZHA_DEV_BAD_SEQUENCE
+                continue
+            if not 0 <= n <= self.t.shape[2] * self.C:
+                bad |= self.zha.ZHA_DEV_BAD_LENGTH
+                continue
+            blocks = -(-n // self.C)
+            if any(e >= 0 and not self._used(e) for e in self.t[s, :, :blocks].flatten()):
+                bad |= self.zha.ZHA_DEV_BAD_PAGE
+                continue
+            need += [(s, h, b) for h in range(self.H) for b in range(blocks) if self.t[s, h, b] < 0]
+        got = self._hand(need)
+        if got is None:
+            bad |= self.zha.ZHA_DEV_NO_PAGES
+        else:
+            for w, p in zip(need, got):
+                self.t[w], self.r[p] = p, 1
+        st = _status()
+        dev = lambda x, dt: torch.tensor(x, dtype=dt, device="cuda")
+        self.zha.pages_extend(self.cfg, self.pool, dev(seqs, torch.int32), dev(tokens, torch.int64), status=st)
+        assert int(st) == bad
+        self.same()
+        return bad
+
+    def fork(self, src, dst, tokens):
+        bad, need, go = 0, [], []
+        for i, (a, b, n) in enumerate(zip(src, dst, tokens)):
+            if not 0 <= b < len(self.t) or b in dst[:i] or not 0 <= a < len(self.t) or a in dst:
+                bad |= self.zha.ZHA_DEV_BAD_SEQUENCE
+                continue
+            if not 0 <= n <= self.t.shape[2] * self.C:
+                bad |= self.zha.ZHA_DEV_BAD_LENGTH
+                continue
+            if (self.t[b] >= 0).any():
+                bad |= self.zha.ZHA_DEV_BAD_SEQUENCE
+                continue
+            if not all(self._used(e) for e in self.t[a, :, : -(-n // self.C)].flatten()):
+                bad |= self.zha.ZHA_DEV_BAD_PAGE
+                continue
+            go.append((a, b, n))
+            need += [(a, b, h, n) for h in range(self.H) if n % self.C]
+        got = self._hand(need)
+        if got is None:
+            bad |= self.zha.ZHA_DEV_NO_PAGES
+        else:
+            for a, b, n in go:
+                f = n // self.C
+                self.t[b, :, :f] = self.t[a, :, :f]
+                for e in self.t[b, :, :f].flatten():
+                    self.r[e] += 1
+            for (a, b, h, n), p in zip(need, got):
+                f, m = n // self.C, n % self.C
+                self.t[b, h, f], self.r[p] = p, 1
+                self.k[p, :m], self.v[p, :m] = self.k[self.t[a, h, f], :m], self.v[self.t[a, h, f], :m]
+        st = _status()
+        dev = lambda x, dt: torch.tensor(x, dtype=dt, device="cuda")
+        self.zha.pages_fork(self.cfg, self.pool, dev(src, torch.int32), dev(dst, torch.int32), dev(tokens, torch.int64),
+                            status=st)
+        assert int(st) == bad
+        self.same()
+        return bad
+
+    def free(self, seqs, keep=None):
+        bad = 0
+        for i, s in enumerate(seqs):
+            n = 0 if keep is None else keep[i]
+            if n < 0:
+                bad |= self.zha.ZHA_DEV_BAD_LENGTH
+                continue
+            if not 0 <= s < len(self.t):
+                bad |= self.zha.ZHA_DEV_BAD_SEQUENCE
+                continue
+            for w in np.ndindex(self.H, self.t.shape[2]):
+                if w[1] >= -(-n // self.C) and self.t[s][w] >= 0:
+                    if self._used(self.t[s][w]):
+                        self.r[self.t[s][w]] -= 1
+                    else:
+                        bad |= self.zha.ZHA_DEV_BAD_PAGE
+                    self.t[s][w] = -1
+        st = _status()
+        dev = lambda x, dt: torch.tensor(x, dtype=dt, device="cuda")
+        self.zha.pages_free(self.cfg, self.pool, dev(seqs, torch.int32),
+                            None if keep is None else dev(keep, torch.int64), status=st)
+        assert int(st) == bad
+        self.same()
+        return bad
+
+    def compact(self):
+        live = [p for p in range(len(self.r)) if self.r[p] > 0]
+        n = len(live)
+        name = {p: p for p in live if p < n}
+        for p, to in zip([p for p in live if p >= n], [p for p in range(n) if self.r[p] <= 0]):
+            name[p] = to
+            self.k[to], self.v[to] = self.k[p], self.v[p]
+            self.r[to], self.r[p] = self.r[p], 0
+        bad = 0
+        for w in np.ndindex(self.t.shape):
+            e = self.t[w]
+            if 0 <= e < len(self.r):
+                self.t[w] = name.get(e, -1)
+                if e not in name:
+                    bad |= self.zha.ZHA_DEV_BAD_PAGE
+        pm, nl, st = torch.full_like(self.refs, 99), _status(), _status()
+        self.zha.pages_compact(self.cfg, self.pool, page_map=pm, n_live=nl, status=st)
+        assert int(st) == bad and int(nl) == n
+        assert pm.tolist() == [name.get(p, -1) for p in range(len(self.r))]
+        self.same()
+        return bad
+
+
+def _lens(p):
+    return [(p.t[s, 0] >= 0).sum() for s in range(len(p.t))]
+
+
+@pytest.mark.parametrize("seed,S,H,C,blocks,pages,d,dt", [(0, 6, 2, 4, 5, 40, 64, F32), (1, 12, 1, 16, 3, 20, 128, BF),
+                                                         (2, 5, 3, 7, 9, 4500, 64, BF), (3, 40, 4, 2, 300, 9000, 64, F32)])
+def test_pages_random_runs_match_the_model(zha, seed, S, H, C, blocks, pages, d, dt):
+    rng = np.random.default_rng(seed)
+    p = Pages(zha, S, H, C, blocks, pages, d, dt, seed)
+    most = blocks * C
+    for _ in range(25):
+        n_items = int(rng.integers(1, S + 1))
+        pick = [int(x) for x in rng.integers(-1, S + 1, n_items)] if rng.random() < 0.3 else [
+            int(x) for x in rng.permutation(S)[:n_items]]
+        tok = [int(x) for x in rng.integers(0 if rng.random() < 0.8 else -2, most + 1, n_items)]
+        op = rng.random()
+        if op < 0.35:
+            p.extend(pick, tok)
+        elif op < 0.6:
+            used = _lens(p)
+            src = [int(rng.integers(0, S)) for _ in pick]
+            tok = [int(rng.integers(0, max(1, used[s] * C + 1))) for s in src]
+            p.fork(src, pick, tok)
+        elif op < 0.9:
+            p.free(pick, None if rng.random() < 0.5 else tok)
+        else:
+            p.compact()
+    p.compact()
+    p.free(list(range(S)))
+    assert (p.t < 0).all() and (p.r == 0).all()
+    p.compact()
+
+
+def test_pages_all_or_nothing_refusals_and_edges(zha):
+    z = zha
+    p = Pages(z, 4, 2, 4, 4, 10)
+    assert p.extend([0], [16]) == 0 and p.t[0].tolist() == [[0, 1, 2, 3], [4, 5, 6, 7]]
+    assert p.extend([1, 2], [4, 1]) == z.ZHA_DEV_NO_PAGES                      # 4 needed, 2 free
+    assert p.extend([1, 1, 9, 2], [4, 4, 4, 17]) == z.ZHA_DEV_BAD_SEQUENCE | z.ZHA_DEV_BAD_LENGTH
+    assert p.t[1, :, 0].tolist() == [8, 9]
+    assert p.extend([1], [0]) == 0 and p.extend([0, 1], [16, 4]) == 0            # nothing new needed
+    assert p.fork([0], [2], [15]) == z.ZHA_DEV_NO_PAGES
+    assert p.fork([0, 1, 2], [2, 1, 3], [12, 4, 0]) == z.ZHA_DEV_BAD_SEQUENCE     # src = dst, src is a destination
+    assert p.r[0] == 2
+    assert p.fork([1], [2], [4]) == z.ZHA_DEV_BAD_SEQUENCE                        # not empty
+    assert p.fork([1], [3], [5]) == z.ZHA_DEV_BAD_PAGE                            # more than it has
+    assert p.free([2, 2, -1, 4], [12, 5, 0, 0]) == z.ZHA_DEV_BAD_SEQUENCE         # twice: the smaller count
+    assert p.t[2].tolist() == [[0, 1, -1, -1], [4, 5, -1, -1]]
+    assert p.free([2, 0], [-1, 16]) == z.ZHA_DEV_BAD_LENGTH
+    assert p.free([0, 2]) == 0
+    assert p.compact() == 0 and p.t[1, :, 0].tolist() == [0, 1]
+    p.t[3, 0, :3] = [5, 0, 1 << 30]                                              # not in use; shared; outside
+    p.put()
+    assert p.extend([3], [4]) == z.ZHA_DEV_BAD_PAGE
+    assert p.fork([3], [2], [4]) == z.ZHA_DEV_BAD_PAGE
+    assert p.compact() == z.ZHA_DEV_BAD_PAGE and p.t[3, 0].tolist() == [-1, 0, 1 << 30, -1]
+    assert p.free([3]) == z.ZHA_DEV_BAD_PAGE
+
+
+def test_pages_captured_with_one_workspace(zha):
+    """Free, fork and extend as one step of a beam search, captured and replayed on
+    other lists, in one workspace."""
+    p = Pages(zha, 6, 2, 4, 6, 80, seed=5)
+    p.extend([0, 1, 2, 3], [9, 14, 3, 8])
+    dev = lambda x, dt: torch.tensor(x, dtype=dt, device="cuda")
+    src, dst = dev([0, 1], torch.int32), dev([2, 3], torch.int32)
+    n, every, new = dev([9, 14], torch.int64), dev([0, 1, 2, 3], torch.int32), dev([10, 15, 10, 15], torch.int64)
+    ws = torch.empty(zha.pages_workspace_bytes(p.cfg, p.pool, 4), dtype=torch.uint8, device="cuda")
+    st = _status()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zha.pages_free(p.cfg, p.pool, dst, ws=ws, status=st)
+        zha.pages_fork(p.cfg, p.pool, src, dst, n, ws=ws, status=st)
+        zha.pages_extend(p.cfg, p.pool, every, new, ws=ws, status=st)
+    twin = Pages(zha, 6, 2, 4, 6, 80, seed=5)
+    twin.extend([0, 1, 2, 3], [9, 14, 3, 8])
+    for s, d, m, grown in (([0, 1], [2, 3], [9, 14], [10, 15, 10, 15]), ([2, 0], [1, 3], [10, 10], [11, 11, 11, 11])):
+        for t, v in ((src, s), (dst, d), (n, m), (new, grown)):
+            t.copy_(torch.tensor(v))
+        ws.fill_(255)
+        graph.replay()
+        twin.free(d)
+        twin.fork(s, d, m)
+        twin.extend([0, 1, 2, 3], grown)
+        p.t, p.r, p.k, p.v = twin.t, twin.r, twin.k, twin.v
+        p.same()
+        assert int(st) == 0
+    with pytest.raises(ValueError):
+        zha.pages_extend(p.cfg, p.pool, every.long(), new)
+    with pytest.raises(ValueError):
+        zha.pages_extend(p.cfg, p.pool, every, new[:2])
+    with pytest.raises(zha.ZhaError):
+        zha.pages_extend(p.cfg, p.pool, every, new, ws=ws[:64])
+
+
+# ---------------------------------------------------------------------------
+# Together
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("cache,q", [(BF, F32), (F32, F32), (BF, BF)])
+def test_a_serving_run_of_the_operators_together(zha, cache, q):
+    """Prompts written, two beams forked, each written further on its own pages, the pool
+    compacted, and attention over what came of it, against plain tensors."""
+    H, G, d, C, S = 2, 4, 64, 16, 4
+    cfg = _cfg(zha, H, G, d, C, cache)
+    pages = 60
+    K = torch.zeros(pages, C, d, dtype=cache, device="cuda")
+    V = torch.zeros_like(K)
+    table = torch.full((S, H, 8), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    pool, kv = zha.page_pool(K, V, table, refs), zha.kv_batch(K, V, table)
+    rope = zha.Rope(d, 24, "half")
+    g = _gen(40)
+    st = _status()
+    dev = lambda x, dt: torch.tensor(x, dtype=dt, device="cuda")
+    keys, values = [[] for _ in range(S)], [[] for _ in range(S)]
+
+    def write(tokens):
+        """tokens: the sequence of each new token, in order."""
+        T = len(tokens)
+        x = torch.randn(T, (G + 2) * H, d, device="cuda", generator=g).to(cache)
+        at = []
+        for t, s in enumerate(tokens):
+            at.append(len(keys[s]))
+            keys[s].append(x[t, G * H:G * H + H])
+            values[s].append(x[t, G * H + H:])
+        now = [len(k) for k in keys]
+        zha.pages_extend(cfg, pool, dev(list(range(S)), torch.int32), dev(now, torch.int64), status=st)
+        return zha.rope_append_kv(cfg, rope, x[:, :G * H], x[:, G * H:G * H + H], x[:, G * H + H:], kv, S,
+                                  dev(tokens, torch.int32), dev(at, torch.int64), q_dtype=q, status=st)
+
+    write([0] * 37 + [3] * 21 + [1] * 5)
+    zha.pages_free(cfg, pool, dev([1], torch.int32), status=st)
+    keys[1], values[1] = list(keys[0]), list(values[0])
+    keys[2], values[2] = list(keys[0][:32]), list(values[0][:32])
+    zha.pages_fork(cfg, pool, dev([0, 0], torch.int32), dev([1, 2], torch.int32), dev([37, 32], torch.int64), status=st)
+    write([1, 0, 2, 0, 1, 2, 3])
+    zha.pages_free(cfg, pool, dev([3], torch.int32), dev([7], torch.int64), status=st)
+    keys[3], values[3] = keys[3][:7], values[3][:7]
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    zha.pages_compact(cfg, pool, n_live=live, status=st)
+    assert int(live) == int((refs > 0).sum()) == int(table.max()) + 1
+    Q = write([0, 1, 2, 3])
+    n = [len(k) for k in keys]
+    out, lse = zha.attend_batch_kv(cfg, Q, kv, S, dev(n, torch.int64), max(n), status=st)
+    assert int(st) == 0
+    b = Batch.__new__(Batch)
+    b.zha, b.S, b.H, b.G, b.d, b.C, b.most, b.K, b.V, b.table, b.Q = zha, S, H, G, d, C, max(n), K, V, table, Q
+    b.n = dev(n, torch.int64)
+    b.check(out, lse)                                  # the attention over the cache as it stands
+    for s in range(S):                                 # and the cache holds what was written
+        for h in range(H):
+            w, tol = _turn64(torch.stack(keys[s]), torch.arange(n[s]), dict(pairs=24, layout="half"))
+            _close(K[b.rows(s, h, n[s])], w[:, h], tol[:, h])
+            assert torch.equal(V[b.rows(s, h, n[s])], torch.stack(values[s])[:, h])
+
+
+def test_dense_attention_is_the_tree_attention_that_keeps_everything(zha):
+    """The two decode paths over one cache: routing with p = 1 keeps every chunk, so the
+    tree's attention over sequence s's table equals the batch call's row s."""
+    b = Batch(zha, [700, 515], 2, 8, 128, 64, BF, F32, seed=41)
+    out, lse = b.run()
+    cfg = zha.make_config(2, 16, 128, 64, 1, 16, BF, 1024)
+    for s, n in enumerate((700, 515)):
+        tree = zha.Tree(cfg, torch.randn(2, 16, 128, device="cuda", generator=_gen(42)))
+        one = zha.kv_cache(b.K, b.V, b.table[s])
+        tree.build_kv(one, n)
+        q = b.Q[s:s + 1]
+        ids, cnt = tree.route(q, n, 1.0, n // 64)
+        assert (cnt == n // 64).all()
+        o, l = tree.sparse_attend_kv(q, one, n, ids, cnt)
+        # both are held to the definition; together twice check()'s bound at these sizes,
+        # which is below 2^-10 for values below 6
+        assert (o[0] - out[s]).abs().max() <= 2.0 ** -10 and (l[0] - lse[s]).abs().max() <= 2.0 ** -10
