@@ -5,13 +5,26 @@
 // log2(e) / sqrt(d): any m gives the same quotient, and states (m, l, o) of two
 // parts of the keys join as m = max, l = sum l_i 2^(m_i - m), o alike.
 //
-// Split. A unit is (sequence, KV head, block of up to 8 of its query heads);
-// its keys are cut into tiles of 64. All units' tiles, one behind the other,
-// are dealt out evenly to the CTAs (CTA c has tiles [c T / n, (c + 1) T / n)),
-// from the counts in device memory, so that ragged lengths cost nothing.
-// A unit that lies in one CTA is finished there; the pieces of the others go to the
-// workspace (piece of CTA c in unit u at slot c + u, so that no two meet) and a
+// Split. A unit is (sequence, KV head, block of its query heads); its keys are cut
+// into tiles of 4 KB of K and 4 KB of V. All units' tiles, one behind the other, are
+// dealt out evenly to the CTAs (CTA c has tiles [c T / n, (c + 1) T / n)), from the
+// counts in device memory, so that ragged lengths cost nothing. A CTA's tiles go
+// round its warps, and each warp keeps its own ring of tiles in flight (cp.async),
+// across the borders of units, so that nothing but the joins makes warps wait for one
+// another. A unit that lies in one CTA is finished there; the pieces of the others go
+// to the workspace (piece of CTA c in unit u at slot c + u, so that no two meet) and a
 // second kernel joins them in a fixed order.
+//
+// Products. A unit has at most 16 query rows, an eighth of a tcgen05 tile, and
+// the call is bound by the cache it reads: the warps' own matrix instructions
+// (16 x 8 x 16 bf16, 16 x 8 x 8 tf32) take their operands from the warp's registers and
+// tile without a hand-over. Their 16 rows hold 8 heads twice, as the first and the
+// following terms of the fp32 operand, or 16 heads.
+//   bf16 cache: keys and values enter exactly. fp32 queries and weights are three
+//   bf16 terms cut off one after the other (8 + 8 + 8 bits: exact); with bf16
+//   queries, which are exact, weights are two terms (2^-16, below the output's 2^-8).
+//   fp32 cache: every operand is two tf32 terms (2^-23), and the product of the
+//   two second terms (2^-24) is left out where 16 heads fill the rows.
 #include <cmath>
 
 #include "zha_host.cuh"
@@ -21,27 +34,30 @@ namespace zha {
 
 namespace {
 
-constexpr int kTile = 64;               // keys per tile
-constexpr int kWarps = 4;               // a tile's keys are split over the warps
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kHeads = 8;               // query heads per unit
-constexpr int kMinTiles = 2;            // no CTA takes less, unless there is less
-constexpr int kMaxCtas = 148 * 4;
+constexpr int kStages = 3;              // tiles in a warp's ring
+constexpr int kTileBytes = 4096;        // of K, and of V
+constexpr int kMaxCtas = 148 * 2;
+constexpr int kSingleTiles = 32;
+
+inline int head_rows(int group) { return group > 8 ? 16 : 8; }
 
 struct BatchLayout {
   int64_t units, slots, bytes, slots_off;
-  int32_t hb;                           // head blocks per KV head
+  int32_t hb, hu;                       // head blocks per KV head, heads per block
 };
 
 // Workspace: int64 prefix[n_seqs + 1] (tiles of one unit of the sequences
-// before s), int32 CTA count; then slots [m, l, 0, 0, o[d]] of 8 heads a piece.
+// before s), int64 CTA count; then slots [m, l, 0, 0, o[d]] of the unit's heads a piece.
 inline BatchLayout batch_layout(const Geom& G, int32_t n_seqs) {
   BatchLayout b{};
-  b.hb = (G.group + kHeads - 1) / kHeads;
+  b.hu = head_rows(G.group);
+  b.hb = (G.group + b.hu - 1) / b.hu;
   b.units = int64_t(n_seqs) * G.hkv * b.hb;
   b.slots = kMaxCtas + b.units;
   b.slots_off = round_up((int64_t(n_seqs) + 2) * 8, 256);
-  b.bytes = b.slots_off + round_up(b.slots * kHeads * (G.d + 4) * 4, 256);
+  b.bytes = b.slots_off + round_up(b.slots * b.hu * (G.d + 4) * 4, 256);
   return b;
 }
 
@@ -55,55 +71,413 @@ struct BatchArgs {
   int64_t* prefix;
   float* slots;
   int32_t* status;
-  int32_t n_seqs, hkv, hq, group, hb, chunk;
+  int32_t n_seqs, hkv, hq, group, hb, chunk, single;
   float scale_log2;                     // log2(e) / sqrt(d)
+};
+
+// ---- small pieces -----------------------------------------------------------
+__device__ __forceinline__ void store_o(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_o(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes into shared memory, or 16 zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The next bf16 term of a pair of values: the upper halves cut off and taken away.
+// (An infinite value has one term.)
+__device__ __forceinline__ uint32_t cut_bf16(float& a, float& b) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  a = a - __uint_as_float(ua & 0xffff0000u);
+  b = b - __uint_as_float(ub & 0xffff0000u);
+  return __byte_perm(ua, ub, 0x7632);
+}
+// The next tf32 term of a value, rounded and taken away.
+__device__ __forceinline__ uint32_t cut_tf32(float& a) {
+  uint32_t t;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(t) : "f"(a));
+  a -= __uint_as_float(t);
+  return t;
+}
+
+// ---- tiles ------------------------------------------------------------------
+// Shared memory keeps a row's 16-byte pieces at piece ^ swizzle(row), so that the
+// reads below meet no bank twice: a K read takes four adjacent pieces of two rows per 8
+// lanes; a V read takes one piece of 8 rows (bf16), or two of every second row (fp32).
+template <typename Kv, int D>
+struct Tile {
+  static constexpr int kRow = D * int(sizeof(Kv));
+  static constexpr int kKeys = kTileBytes / kRow;         // bf16: 16 or 32; fp32: 8 or 16
+  static constexpr int kPieces = kRow / 16;               // 8, 16 or 32
+  __device__ static int at_k(int row, int piece) { return row * kRow + ((piece ^ ((row & 1) << 2)) << 4); }
+  __device__ static int at_v(int row, int piece) { return row * kRow + ((piece ^ (row & 7)) << 4); }
+};
+
+// A place in the row of tiles: unit (s, ub) of sequence s with n tokens has the
+// tiles [first, end).
+struct Place {
+  int64_t first, end, n;
+  int s, ub;
 };
 
 __device__ __forceinline__ int64_t clamped(const BatchArgs& A, int s) {
   return max64(0, min64(A.n_tokens[s], A.max_tokens));
 }
-__device__ __forceinline__ int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+template <int KEYS>
+__device__ __forceinline__ int64_t tiles_of(int64_t n) { return (n + KEYS - 1) / KEYS; }
 
-template <typename T>
-__device__ __forceinline__ float load_q(const T* p) { return float(*p); }
+// To the next unit that has tiles; the caller knows that there is one.
+template <int KEYS>
+__device__ __forceinline__ void next_unit(const BatchArgs& A, Place& p) {
+  if (++p.ub == A.hkv * A.hb) {
+    p.ub = 0;
+    do p.n = clamped(A, ++p.s); while (p.n == 0);
+  }
+  p.first = p.end;
+  p.end += tiles_of<KEYS>(p.n);
+}
 
-__device__ __forceinline__ void store_o(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_o(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// A warp's query rows as matrix operands. Lane (g, t) = (lane / 4, lane % 4)
+// has rows g and g + 8; the order of the head's elements within a step is that of the K
+// reads: lane t's piece of 16 bytes serves two steps.
+template <typename Kv, typename Qt, int D, int HU>
+struct Queries;
 
-template <typename Kv, typename Qt, int D>
-__global__ void __launch_bounds__(kThreads) attend_batch_kernel(const BatchArgs A) {
-  constexpr int EPL = D / 32;
-  __shared__ int64_t s_scan[kThreads];
-  __shared__ int64_t s_at[3];                        // sequence, its first tile, total
-  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
-  __shared__ float s_o[kWarps][kHeads][D];
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+template <typename Qt, int D, int HU>
+struct Queries<__nv_bfloat16, Qt, D, HU> {
+  static constexpr bool kExact = sizeof(Qt) == 2;          // one term
+  static constexpr int kSteps = D / 16;
+  static constexpr int kMore = kExact ? 0 : HU == 16 ? 4 : 1;
+  uint32_t a[kSteps][HU == 16 ? 4 : kExact ? 2 : 4];       // first terms of rows g, g + 8 (HU 8: rows g; second terms)
+  uint32_t b[kSteps][kMore == 0 ? 1 : kMore * (HU == 16 ? 1 : 2)];   // HU 16: second, third terms; HU 8: third
+
+  __device__ void load(const Qt* q, int heads, int lane) {
+    const int g = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int r = 0; r < HU / 8; ++r) {
+      const int h = g + 8 * r;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        float v[8] = {};
+        if (h < heads) {
+          if constexpr (kExact) {
+            load_slice<8>(q + h * D, 32 * j + 8 * t, v);
+          } else {
+            float x[4], y[4];
+            load_slice<4>(q + h * D, 32 * j + 8 * t, x);
+            load_slice<4>(q + h * D, 32 * j + 8 * t + 4, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { v[i] = x[i]; v[4 + i] = y[i]; }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                        // step 2j + i / 2, first or second half of its elements
+          const int st = 2 * j + i / 2, hi = i % 2;
+          const uint32_t one = cut_bf16(v[2 * i], v[2 * i + 1]);
+          if constexpr (kExact) {
+            a[st][HU == 16 ? r + 2 * hi : hi] = one;
+          } else {
+            const uint32_t two = cut_bf16(v[2 * i], v[2 * i + 1]), three = cut_bf16(v[2 * i], v[2 * i + 1]);
+            if constexpr (HU == 16) {
+              a[st][r + 2 * hi] = one;
+              b[st][r + 2 * hi] = two;
+              c[st][r + 2 * hi] = three;
+            } else {
+              a[st][2 * hi] = one;
+              a[st][2 * hi + 1] = two;
+              b[st][hi] = three;
+            }
+          }
+        }
+      }
+    }
+  }
+  uint32_t c[kSteps][kMore == 4 ? 4 : 1];
+
+  // s[n tile][2 r + e]: row g + 8 r, key 8 * tile + 2 t + e.
+  template <int NT>
+  __device__ void scores(const char* tile, int lane, float (&s)[NT][4]) const {
+    const int g = lane / 4, t = lane % 4;
+    float low[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = low[n][i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 k = *reinterpret_cast<const uint4*>(tile + Tile<__nv_bfloat16, D>::at_k(8 * n + g, 4 * j + t));
+        const uint32_t kb[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int st = 2 * j + u;
+          if constexpr (HU == 16) {
+            mma_bf16(s[n], a[st][0], a[st][1], a[st][2], a[st][3], kb[2 * u], kb[2 * u + 1]);
+            if constexpr (!kExact) {
+              mma_bf16(low[n], b[st][0], b[st][1], b[st][2], b[st][3], kb[2 * u], kb[2 * u + 1]);
+              mma_bf16(low[n], c[st][0], c[st][1], c[st][2], c[st][3], kb[2 * u], kb[2 * u + 1]);
+            }
+          } else if constexpr (kExact) {
+            mma_bf16(s[n], a[st][0], 0u, a[st][1], 0u, kb[2 * u], kb[2 * u + 1]);
+          } else {
+            mma_bf16(s[n], a[st][0], a[st][1], a[st][2], a[st][3], kb[2 * u], kb[2 * u + 1]);
+            mma_bf16(s[n], 0u, b[st][0], 0u, b[st][1], kb[2 * u], kb[2 * u + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (HU == 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
+      } else {
+        s[n][0] += s[n][2];
+        s[n][1] += s[n][3];
+      }
+    }
+  }
+};
+
+template <typename Qt, int D, int HU>
+struct Queries<float, Qt, D, HU> {
+  static constexpr int kSteps = D / 8;
+  uint32_t a[kSteps][4];                                     // HU 8: rows g first terms, rows g + 8 second terms
+  uint32_t b[HU == 16 ? kSteps : 1][4];                      // HU 16: second terms
+
+  __device__ void load(const Qt* q, int heads, int lane) {
+    const int g = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int r = 0; r < HU / 8; ++r) {
+      const int h = g + 8 * r;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        float v[4] = {};
+        if (h < heads) load_slice<4>(q + h * D, 16 * j + 4 * t, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int st = 2 * j + i / 2, hi = i % 2;
+          const uint32_t one = cut_tf32(v[i]), two = cut_tf32(v[i]);
+          a[st][2 * hi + r] = one;
+          if constexpr (HU == 16) b[st][2 * hi + r] = two;
+          else a[st][2 * hi + 1] = two;
+        }
+      }
+    }
+  }
+
+  template <int NT>
+  __device__ void scores(const char* tile, int lane, float (&s)[NT][4]) const {
+    const int g = lane / 4, t = lane % 4;
+    float low[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = low[n][i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4 k = *reinterpret_cast<const float4*>(tile + Tile<float, D>::at_k(8 * n + g, 4 * j + t));
+        float kr[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int st = 2 * j + u;
+          const uint32_t h0 = cut_tf32(kr[2 * u]), h1 = cut_tf32(kr[2 * u + 1]);
+          const uint32_t l0 = cut_tf32(kr[2 * u]), l1 = cut_tf32(kr[2 * u + 1]);
+          mma_tf32(s[n], a[st][0], a[st][1], a[st][2], a[st][3], h0, h1);
+          mma_tf32(low[n], a[st][0], a[st][1], a[st][2], a[st][3], l0, l1);
+          if constexpr (HU == 16) mma_tf32(low[n], b[st][0], b[st][1], b[st][2], b[st][3], h0, h1);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
+      if constexpr (HU == 8) {
+        s[n][0] += s[n][2];
+        s[n][1] += s[n][3];
+      }
+    }
+  }
+};
+
+// o[n tile] += weights * V. p[n tile][2 r + e] as the scores.
+template <int D, int HU, int TERMS, int NT>
+__device__ __forceinline__ void add_values(const __nv_bfloat16*, uint32_t tile, const char*, int lane, float (&p)[NT][4],
+                                           float (&o)[D / 8][4]) {
+#pragma unroll
+  for (int kb = 0; kb < NT / 2; ++kb) {
+    uint32_t w[TERMS][4];                                    // [term][element half * 2 + row]: a0..a3 of 16 rows
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int r = 0; r < HU / 8; ++r)
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) w[k][2 * half + r] = cut_bf16(p[2 * kb + half][2 * r], p[2 * kb + half][2 * r + 1]);
+    const int row = kb * 16 + (lane & 15);
+#pragma unroll
+    for (int np = 0; np < D / 16; ++np) {
+      uint32_t v0, v1, v2, v3;
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3)
+                   : "r"(tile + Tile<__nv_bfloat16, D>::at_v(row, 2 * np + (lane >> 4)))
+                   : "memory");
+      if constexpr (HU == 16) {
+#pragma unroll
+        for (int k = TERMS - 1; k >= 0; --k) {
+          mma_bf16(o[2 * np], w[k][0], w[k][1], w[k][2], w[k][3], v0, v1);
+          mma_bf16(o[2 * np + 1], w[k][0], w[k][1], w[k][2], w[k][3], v2, v3);
+        }
+      } else {
+        if constexpr (TERMS == 3) {
+          mma_bf16(o[2 * np], 0u, w[2][0], 0u, w[2][2], v0, v1);
+          mma_bf16(o[2 * np + 1], 0u, w[2][0], 0u, w[2][2], v2, v3);
+        }
+        mma_bf16(o[2 * np], w[0][0], w[1][0], w[0][2], w[1][2], v0, v1);
+        mma_bf16(o[2 * np + 1], w[0][0], w[1][0], w[0][2], w[1][2], v2, v3);
+      }
+    }
+  }
+}
+
+// fp32: within a tile of 8 keys, the step's elements t and t + 4 are the keys 2 t and
+// 2 t + 1, which is how the scores lie.
+template <int D, int HU, int TERMS, int NT>
+__device__ __forceinline__ void add_values(const float*, uint32_t, const char* tile, int lane, float (&p)[NT][4],
+                                           float (&o)[D / 8][4]) {
+  const int g = lane / 4, t = lane % 4;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    uint32_t w[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int r = 0; r < HU / 8; ++r) {
+        w[0][2 * e + r] = cut_tf32(p[n][2 * r + e]);
+        w[1][2 * e + r] = cut_tf32(p[n][2 * r + e]);
+      }
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const float4 x = *reinterpret_cast<const float4*>(tile + Tile<float, D>::at_v(8 * n + 2 * t, 8 * j + g));
+      const float4 y = *reinterpret_cast<const float4*>(tile + Tile<float, D>::at_v(8 * n + 2 * t + 1, 8 * j + g));
+      float vx[4] = {x.x, x.y, x.z, x.w}, vy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t h0 = cut_tf32(vx[i]), h1 = cut_tf32(vy[i]), l0 = cut_tf32(vx[i]), l1 = cut_tf32(vy[i]);
+        float(&c)[4] = o[4 * j + i];
+        if constexpr (HU == 16) {
+          mma_tf32(c, w[0][0], w[0][1], w[0][2], w[0][3], l0, l1);
+          mma_tf32(c, w[1][0], w[1][1], w[1][2], w[1][3], h0, h1);
+          mma_tf32(c, w[0][0], w[0][1], w[0][2], w[0][3], h0, h1);
+        } else {
+          mma_tf32(c, w[0][0], w[1][0], w[0][2], w[1][2], l0, l1);
+          mma_tf32(c, w[0][0], w[1][0], w[0][2], w[1][2], h0, h1);
+        }
+      }
+    }
+  }
+}
+
+// The head's element in column 2 t + e of o's n tile.
+template <typename Kv>
+__device__ __forceinline__ int element_of(int tile, int col) {
+  return sizeof(Kv) == 2 ? tile * 8 + col : (tile / 4) * 32 + col * 4 + tile % 4;
+}
+
+template <int D>
+struct JoinSmem {
+  float o[kWarps][8][D];
+  float m[kWarps][8], l[kWarps][8];
+  uint32_t mask[kWarps][kStages];                            // keys of a tile that are there
+  int64_t scan[kWarps], at[2];
+};
+constexpr size_t batch_smem(int d) { return size_t(kWarps) * kStages * 2 * kTileBytes + (d == 128 ? sizeof(JoinSmem<128>) : sizeof(JoinSmem<64>)); }
+
+template <typename Kv, typename Qt, int D, int HU>
+__global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchArgs A) {
+  using T = Tile<Kv, D>;
+  constexpr int KEYS = T::kKeys, NT = KEYS / 8, NH = HU / 8;
+  constexpr int TERMS = sizeof(Kv) == 4 || sizeof(Qt) == 2 ? 2 : 3;
+  extern __shared__ __align__(128) char smem[];
+  JoinSmem<D>& J = *reinterpret_cast<JoinSmem<D>*>(smem + kWarps * kStages * 2 * kTileBytes);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
+  char* ring = smem + warp * kStages * 2 * kTileBytes;
+  const uint32_t ring_at = uint32_t(__cvta_generic_to_shared(ring));
   pdl_trigger();
   pdl_wait();
 
-  // Tiles of all sequences and where this CTA's begin. Thread i scans a run of
-  // ceil(S / 128) sequences.
-  const int run = (A.n_seqs + kThreads - 1) / kThreads;
-  const int s0 = min(A.n_seqs, tid * run), s1 = min(A.n_seqs, s0 + run);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += tiles_of(clamped(A, s));
-  s_scan[tid] = mine;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int i = 0; i < kThreads; ++i) {
-    if (i < tid) before += s_scan[i];
-    all += s_scan[i];
-  }
-  const int64_t per = int64_t(A.hkv) * A.hb;         // units of a sequence
-  const int64_t T = all * per;
-  const int64_t n_cta = max64(1, min64(gridDim.x, (T + kMinTiles - 1) / kMinTiles));
-  const int64_t c = blockIdx.x;
-  const int64_t t0 = c < n_cta ? c * T / n_cta : T, t1 = c < n_cta ? (c + 1) * T / n_cta : T;
-  {
-    int64_t at = before;
+  const int per = A.hkv * A.hb;                              // units of a sequence
+  int64_t t0, t1;
+  Place cur;
+  if (A.single) {                                            // one unit a CTA
+    cur.s = blockIdx.x / per;
+    cur.ub = blockIdx.x - cur.s * per;
+    const int64_t n = A.n_tokens[cur.s];
+    if (tid == 0 && cur.ub == 0 && (n < 0 || n > A.max_tokens) && A.status != nullptr)
+      atomicOr(A.status, ZHA_DEV_BAD_LENGTH);
+    cur.n = clamped(A, cur.s);
+    cur.first = t0 = 0;
+    cur.end = t1 = tiles_of<KEYS>(cur.n);
+    if (cur.n == 0) {
+      const int h0 = (cur.ub % A.hb) * HU, heads = min(HU, A.group - h0);
+      const int64_t qrow = int64_t(cur.s) * A.hq + int64_t(cur.ub / A.hb) * A.group + h0;
+      for (int i = tid; i < heads * D; i += kThreads) store_o(static_cast<Qt*>(A.O) + qrow * D + i, 0.f);
+      if (tid < heads && A.lse != nullptr) A.lse[qrow + tid] = -INFINITY;
+      return;
+    }
+  } else {
+    // Tiles of all sequences and where this CTA's begin. Thread i scans a run of
+    // ceil(S / threads) sequences.
+    const int run = (A.n_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(A.n_seqs, tid * run), s1 = min(A.n_seqs, s0 + run);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) mine += tiles_of<KEYS>(clamped(A, s));
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) J.scan[warp] = upto;
+    __syncthreads();
+    int64_t at = upto - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += J.scan[w];
+      all += J.scan[w];
+    }
+    const int64_t total = all * per;
+    const int64_t c = blockIdx.x, n_cta = max64(1, min64(gridDim.x, (total + kWarps - 1) / kWarps));
+    t0 = c < n_cta ? c * total / n_cta : total;
+    t1 = c < n_cta ? (c + 1) * total / n_cta : total;
     for (int s = s0; s < s1; ++s) {
-      const int64_t n = A.n_tokens[s], tl = tiles_of(clamped(A, s));
-      if (t0 >= at * per && t0 < (at + tl) * per) { s_at[0] = s; s_at[1] = at; }
+      const int64_t n = A.n_tokens[s], tl = tiles_of<KEYS>(clamped(A, s));
+      if (t0 >= at * per && t0 < (at + tl) * per) { J.at[0] = s; J.at[1] = at; }
       if (c == 0) {
         A.prefix[s] = at;
         if ((n < 0 || n > A.max_tokens) && A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_LENGTH);
@@ -111,96 +485,173 @@ __global__ void __launch_bounds__(kThreads) attend_batch_kernel(const BatchArgs 
       at += tl;
     }
     if (c == 0 && tid == 0) { A.prefix[A.n_seqs] = all; A.prefix[A.n_seqs + 1] = n_cta; }
+    __syncthreads();
+    if (t0 >= t1) return;
+    cur.s = int(J.at[0]);
+    cur.n = clamped(A, cur.s);
+    const int64_t tl = tiles_of<KEYS>(cur.n), base = J.at[1] * per;
+    cur.ub = int((t0 - base) / tl);
+    cur.first = base + cur.ub * tl;
+    cur.end = cur.first + tl;
   }
-  __syncthreads();
-  if (t0 >= t1) return;
-  int s = int(s_at[0]);
-  int64_t seq_tile = s_at[1];
 
-  int64_t t = t0;
-  while (t < t1) {
-    const int64_t n = clamped(A, s), tl = tiles_of(n);
-    if (tl == 0 || t >= (seq_tile + tl) * per) { seq_tile += tl; ++s; continue; }
-    const int64_t local = t - seq_tile * per;
-    const int ub = int(local / tl);
-    const int64_t first = seq_tile * per + int64_t(ub) * tl;      // the unit's first tile
-    const int64_t stop = min64(t1, first + tl);
-    const int g = ub / A.hb, h0 = (ub % A.hb) * kHeads, heads = min(kHeads, A.group - h0);
-    const int64_t qrow = int64_t(s) * A.hq + int64_t(g) * A.group + h0;
+  // The ring. `row` is the cache row of the next tile's key `lane`, looked up one
+  // tile ahead of its copy; -1: absent.
+  Place ahead = cur;
+  int64_t next = t0 + warp;
+  int32_t row = -1;
+  auto look_up = [&] {
+    row = -1;
+    if (next >= t1) return;
+    while (next >= ahead.end) next_unit<KEYS>(A, ahead);
+    const int64_t tok = (next - ahead.first) * KEYS + lane;
+    if (lane < KEYS && tok < ahead.n) {
+      row = kv_batch_row(A.kv, A.hkv, ahead.s, ahead.ub / A.hb, tok, A.chunk);
+      if (row < 0 && A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_PAGE);
+    }
+  };
+  auto issue = [&](int stage) {
+    if (next < t1) {
+      const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
+      if (lane == 0) J.mask[warp][stage] = mask;
+      const uint32_t to = ring_at + stage * 2 * kTileBytes;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int key = (i * 32 + lane) / T::kPieces, piece = lane % T::kPieces;
+        const int32_t r = __shfl_sync(0xffffffffu, row, key);
+        const int64_t off = int64_t(max(r, 0)) * T::kRow + piece * 16;
+        copy16(to + T::at_k(key, piece), static_cast<const char*>(A.kv.k) + off, r >= 0);
+        copy16(to + kTileBytes + T::at_v(key, piece), static_cast<const char*>(A.kv.v) + off, r >= 0);
+      }
+      next += kWarps;
+      look_up();
+    }
+    copy_commit();
+  };
+  look_up();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-    float q[kHeads][EPL], o[kHeads][EPL], m[kHeads], l[kHeads];
+  int64_t at = t0 + warp;
+  int stage = 0;
+  while (true) {
+    const int h0 = (cur.ub % A.hb) * HU, heads = min(HU, A.group - h0);
+    const int64_t qrow = int64_t(cur.s) * A.hq + int64_t(cur.ub / A.hb) * A.group + h0;
+    Queries<Kv, Qt, D, HU> q;
+    q.load(static_cast<const Qt*>(A.Q) + qrow * D, heads, lane);
+    float m[NH], l[NH], o[D / 8][4];
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      m[h] = -INFINITY; l[h] = 0.f;
+    for (int r = 0; r < NH; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        o[h][e] = 0.f;
-        q[h][e] = h < heads ? load_q(static_cast<const Qt*>(A.Q) + (qrow + h) * D + lane * EPL + e) * A.scale_log2 : 0.f;
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    const int64_t stop = min64(t1, cur.end);
+    for (; at < stop; at += kWarps) {
+      __syncwarp();                                          // the stage that is refilled has been read by all lanes
+      issue(stage == 0 ? kStages - 1 : stage - 1);
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      const char* tile = ring + stage * 2 * kTileBytes;
+      const uint32_t mask = J.mask[warp][stage];
+      float p[NT][4];
+      q.scores(tile, lane, p);
+      float top[NH];
+#pragma unroll
+      for (int r = 0; r < NH; ++r) {
+        top[r] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = p[n][2 * r + e];
+            x = (mask >> (8 * n + 2 * t4 + e)) & 1u ? x * A.scale_log2 : -INFINITY;
+            top[r] = fmaxf(top[r], x);
+          }
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
       }
-    }
-    for (int64_t tile = t - first; tile < stop - first; ++tile) {
-      for (int i = 0; i < kTile / kWarps; ++i) {
-        const int64_t tok = tile * kTile + i * kWarps + warp;
-        if (tok >= n) break;
-        const int32_t row = kv_batch_row(A.kv, A.hkv, s, g, tok, A.chunk);
-        if (row < 0) {
-          if (lane == 0 && A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_PAGE);
-          continue;
-        }
-        float k[EPL], v[EPL];
-        load_slice<EPL>(static_cast<const Kv*>(A.kv.k) + int64_t(row) * D, lane * EPL, k);
-        load_slice<EPL>(static_cast<const Kv*>(A.kv.v) + int64_t(row) * D, lane * EPL, v);
+      bool higher = false;
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          float x = 0.f;
+      for (int r = 0; r < NH; ++r) higher |= top[r] > m[r];
+      if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) x = fmaf(q[h][e], k[e], x);
-          x = warp_sum(x);
-          const float mn = fmaxf(m[h], x), at = mn == -INFINITY ? 0.f : mn, a = exp2f(m[h] - at), p = exp2f(x - at);
-          m[h] = mn;
-          l[h] = l[h] * a + p;
+        for (int r = 0; r < NH; ++r) {
+          const float mn = fmaxf(m[r], top[r]), a = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+          m[r] = mn;
+          l[r] *= a;
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) o[h][e] = fmaf(p, v[e], o[h][e] * a);
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][2 * r] *= a;
+            o[i][2 * r + 1] *= a;
+            if constexpr (HU == 8) { o[i][2] *= a; o[i][3] *= a; }
+          }
         }
       }
+#pragma unroll
+      for (int r = 0; r < NH; ++r) {
+        const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = p[n][2 * r + e];
+            x = ex2(x - base);
+            l[r] += x;
+          }
+      }
+      add_values<D, HU, TERMS, NT>(static_cast<const Kv*>(nullptr), ring_at + stage * 2 * kTileBytes + kTileBytes,
+                                   tile + kTileBytes, lane, p, o);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
+
     // The warps' states joined, in warp order.
-    __syncthreads();
+    const bool whole = t0 <= cur.first && cur.end <= t1;
+    const int64_t unit = int64_t(cur.s) * per + cur.ub;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      if (lane == 0) { s_m[warp][h] = m[h]; s_l[warp][h] = l[h]; }
+    for (int r = 0; r < NH; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      __syncthreads();
+      if (t4 == 0) { J.m[warp][g] = m[r]; J.l[warp][g] = l[r]; }
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) s_o[warp][h][lane * EPL + e] = o[h][e];
-    }
-    __syncthreads();
-    const bool whole = t == first && stop == first + tl;
-    const int64_t unit = int64_t(s) * per + ub;
-    for (int i = tid; i < heads * D; i += kThreads) {
-      const int h = i / D, e = i % D;
-      float M = -INFINITY;
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
-      float L = 0.f, acc = 0.f;
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = s_l[w][h] > 0.f || isnan(s_l[w][h]) ? exp2f(s_m[w][h] - M) : 0.f;
-        L += s_l[w][h] * f;
-        acc += s_o[w][h][e] * f;
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          J.o[warp][g][element_of<Kv>(i, 2 * t4 + e)] = HU == 8 ? o[i][e] + o[i][2 + e] : o[i][2 * r + e];
+      __syncthreads();
+      const int mine = min(8, heads - 8 * r);
+      for (int i = tid; i < mine * D; i += kThreads) {
+        const int h = i / D, e = i % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, J.m[w][h]);
+        float L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float lw = J.l[w][h], f = lw != 0.f ? ex2(J.m[w][h] - M) : 0.f;
+          L += lw * f;
+          acc += J.o[w][h][e] * f;
+        }
+        const int64_t out = qrow + 8 * r + h;
+        if (whole) {
+          store_o(static_cast<Qt*>(A.O) + out * D + e, L == 0.f ? 0.f : acc / L);
+          if (e == 0 && A.lse != nullptr) A.lse[out] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
+        } else {
+          float* slot = A.slots + ((blockIdx.x + unit) * HU + 8 * r + h) * (D + 4);
+          slot[4 + e] = acc;
+          if (e == 0) { slot[0] = M; slot[1] = L; }
+        }
       }
-      if (whole) {
-        store_o(static_cast<Qt*>(A.O) + (qrow + h) * D + e, L == 0.f ? 0.f : acc / L);
-        if (e == 0 && A.lse != nullptr) A.lse[qrow + h] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
-      } else {
-        float* slot = A.slots + ((c + unit) * kHeads + h) * (D + 4);
-        slot[4 + e] = acc;
-        if (e == 0) { slot[0] = M; slot[1] = L; }
-      }
     }
-    t = stop;
+    if (cur.end >= t1) break;
+    next_unit<KEYS>(A, cur);
   }
+  copy_wait<0>();
 }
 
 // One warp per (sequence, query head): nothing to do for a unit that one CTA
 // finished; zeros for one without tiles; else its pieces joined in CTA order.
-template <typename Qt, int D>
+template <typename Qt, int D, int HU>
 __global__ void __launch_bounds__(kThreads) attend_batch_join_kernel(const BatchArgs A) {
   constexpr int EPL = D / 32;
   const int lane = threadIdx.x % 32;
@@ -209,24 +660,40 @@ __global__ void __launch_bounds__(kThreads) attend_batch_join_kernel(const Batch
   pdl_wait();
   if (row >= int64_t(A.n_seqs) * A.hq) return;
   const int s = int(row / A.hq), qh = int(row % A.hq), g = qh / A.group, hh = qh % A.group;
-  const int64_t per = int64_t(A.hkv) * A.hb, ub = int64_t(g) * A.hb + hh / kHeads;
+  const int64_t per = int64_t(A.hkv) * A.hb, ub = int64_t(g) * A.hb + hh / HU;
   const int64_t seq_tile = A.prefix[s], tl = A.prefix[s + 1] - seq_tile;
-  const int64_t T = A.prefix[A.n_seqs] * per, n_cta = A.prefix[A.n_seqs + 1];
+  const int64_t total = A.prefix[A.n_seqs] * per, n_cta = A.prefix[A.n_seqs + 1];
   float acc[EPL] = {}, M = -INFINITY, L = 0.f;
   if (tl > 0) {
     const int64_t lo = seq_tile * per + ub * tl, hi = lo + tl;
-    const int64_t c0 = ((lo + 1) * n_cta - 1) / T, c1 = (hi * n_cta - 1) / T;
-    if (c0 == c1) return;
-    for (int64_t c = c0; c <= c1; ++c) {
-      const float* slot = A.slots + ((c + s * per + ub) * kHeads + hh % kHeads) * (D + 4);
-      const float m = slot[0], l = slot[1];
-      if (l == 0.f) continue;
-      const float mn = fmaxf(M, m), a = L == 0.f ? 0.f : exp2f(M - mn), b = exp2f(m - mn);
-      M = mn;
-      L = L * a + l * b;
+    const int64_t c0 = ((lo + 1) * n_cta - 1) / total;
+    const int n = int((hi * n_cta - 1) / total - c0) + 1;
+    if (n == 1) return;
+    const float* slots = A.slots + ((c0 + s * per + ub) * HU + hh % HU) * (D + 4);
+    constexpr int64_t step = int64_t(HU) * (D + 4);
+    for (int i = lane; i < n; i += 32)
+      if (slots[i * step + 1] != 0.f) M = fmaxf(M, slots[i * step]);
+    M = warp_max(M);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float w = 0.f;
+      if (i0 + lane < n) {
+        const float l = slots[(i0 + lane) * step + 1];
+        if (l != 0.f) {
+          w = ex2(slots[(i0 + lane) * step] - M);
+          L += l * w;
+        }
+      }
+      const int most = min(32, n - i0);
+#pragma unroll 8
+      for (int i = 0; i < most; ++i) {
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        float x[EPL];
+        load_slice<EPL>(slots + (i0 + i) * step + 4, lane * EPL, x);
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = acc[e] * a + slot[4 + lane * EPL + e] * b;
+        for (int e = 0; e < EPL; ++e) acc[e] = f == 0.f ? acc[e] : fmaf(x[e], f, acc[e]);
+      }
     }
+    L = warp_sum(L);
   }
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
@@ -234,36 +701,43 @@ __global__ void __launch_bounds__(kThreads) attend_batch_join_kernel(const Batch
   if (lane == 0 && A.lse != nullptr) A.lse[row] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
 }
 
-template <typename Kv, typename Qt, int D>
-cudaError_t launch_batch(const BatchArgs& A, cudaStream_t s) {
+template <typename Kv, typename Qt, int D, int HU>
+cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int64_t most = int64_t(A.n_seqs) * A.hkv * A.hb * ((A.max_tokens + kTile - 1) / kTile);
-  const int64_t ctas = max64(1, min64(min64(int64_t(sms) * 4, kMaxCtas), (most + kMinTiles - 1) / kMinTiles));
+  auto kernel = attend_batch_kernel<Kv, Qt, D, HU>;
+  e = ensure_dynamic_smem(kernel, batch_smem(D));
+  if (e != cudaSuccess) return e;
+  const int64_t units = int64_t(A.n_seqs) * A.hkv * A.hb;
+  const int64_t tiles = (A.max_tokens + Tile<Kv, D>::kKeys - 1) / Tile<Kv, D>::kKeys;
+  A.single = tiles <= kSingleTiles && units <= int64_t(sms) * 2;
+  const int64_t ctas = A.single ? units : max64(1, min64(min64(int64_t(sms) * 2, kMaxCtas), (units * tiles + kWarps - 1) / kWarps));
   {
     TraceScope ts("attend_batch_kernel", 0, s);
     zha_count_launch();
-    e = launch_pdl(attend_batch_kernel<Kv, Qt, D>, dim3(unsigned(ctas)), dim3(kThreads), 0, s, A);
+    e = launch_pdl(kernel, dim3(unsigned(ctas)), dim3(kThreads), batch_smem(D), s, A);
     if (e != cudaSuccess) return e;
   }
+  if (A.single) return cudaSuccess;
   TraceScope ts("attend_batch_join_kernel", 0, s);
   zha_count_launch();
   const int64_t rows = int64_t(A.n_seqs) * A.hq;
-  return launch_pdl(attend_batch_join_kernel<Qt, D>, dim3(unsigned((rows + kWarps - 1) / kWarps)), dim3(kThreads), 0,
+  return launch_pdl(attend_batch_join_kernel<Qt, D, HU>, dim3(unsigned((rows + kWarps - 1) / kWarps)), dim3(kThreads), 0,
                     s, A);
 }
 
 template <typename Kv, typename Qt>
 cudaError_t launch_batch_d(const BatchArgs& A, int d, cudaStream_t s) {
-  return d == 128 ? launch_batch<Kv, Qt, 128>(A, s) : launch_batch<Kv, Qt, 64>(A, s);
+  if (head_rows(A.group) == 16) return d == 128 ? launch_batch<Kv, Qt, 128, 16>(A, s) : launch_batch<Kv, Qt, 64, 16>(A, s);
+  return d == 128 ? launch_batch<Kv, Qt, 128, 8>(A, s) : launch_batch<Kv, Qt, 64, 8>(A, s);
 }
 
 // Units beyond this are refused: slots and grids stay far below 2^31.
 constexpr int64_t kMaxUnits = int64_t(1) << 22;
 
 bool units_ok(const Geom& G, int32_t n_seqs) {
-  const int64_t hb = (G.group + kHeads - 1) / kHeads;
+  const int64_t hb = (G.group + head_rows(G.group) - 1) / head_rows(G.group);
   return int64_t(G.hkv) * hb <= kMaxUnits / n_seqs;
 }
 
@@ -296,7 +770,7 @@ zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q
     return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: unknown q_dtype");
   if (d_n_tokens == nullptr) return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: n_tokens is NULL");
   if (!zha::units_ok(G, n_seqs))
-    return zha_report_error(ZHA_ERR_UNSUPPORTED, "zha_attend_batch_kv: more than 2^22 (sequence, KV head, 8-query block) units");
+    return zha_report_error(ZHA_ERR_UNSUPPORTED, "zha_attend_batch_kv: more than 2^22 (sequence, KV head, query block) units");
   const zha::BatchLayout lay = zha::batch_layout(G, n_seqs);
   if (d_ws == nullptr || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0 || int64_t(ws_bytes) < lay.bytes)
     return zha_report_error(ZHA_ERR_CAPACITY,
