@@ -7,13 +7,18 @@
 //
 // Split. A unit is (sequence, KV head, block of its query heads); its keys are cut
 // into tiles of 4 KB of K and 4 KB of V. All units' tiles, one behind the other, are
-// dealt out evenly to the CTAs (CTA c has tiles [c T / n, (c + 1) T / n)), from the
-// counts in device memory, so that ragged lengths cost nothing. A CTA's tiles go
-// round its warps, and each warp keeps its own ring of tiles in flight (cp.async),
-// across the borders of units, so that nothing but the joins makes warps wait for one
-// another. A unit that lies in one CTA is finished there; the pieces of the others go
-// to the workspace (piece of CTA c in unit u at slot c + u, so that no two meet) and a
-// second kernel joins them in a fixed order.
+// dealt out evenly to the warps (warp w has tiles [w T / n, (w + 1) T / n)), from the
+// counts in device memory, so that ragged lengths cost nothing. A warp keeps its own
+// ring of tiles in flight (cp.async), across the borders of units, and waits for no
+// other until its tiles are done. What then becomes of a unit's state:
+//   - all of its tiles in one warp: the warp writes the result;
+//   - it ends before the warp's last tile, having begun in an earlier warp: an end
+//     piece in the workspace, at the warp's number;
+//   - it reaches the warp's last tile: the CTA joins the states of its warps in that
+//     unit, and writes the result or, with more of the unit elsewhere, a group piece, at
+//     the number of the group's first warp.
+// A second kernel finds a unit's pieces from the tile counts alone and joins them in a
+// fixed order.
 //
 // Products. A unit has at most 16 query rows, an eighth of a tcgen05 tile, and
 // the call is bound by the cache it reads: the warps' own matrix instructions
@@ -39,7 +44,11 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;              // tiles in a warp's ring
 constexpr int kTileBytes = 4096;        // of K, and of V
 constexpr int kMaxCtas = 148 * 2;
+constexpr int kMaxWarps = kMaxCtas * kWarps;
+constexpr int kMinTiles = 2;            // no warp takes less, unless there is less
 constexpr int kSingleTiles = 32;
+constexpr int kJoinThreads = 256;
+constexpr int kWideUnits = 148;        // up to so many units a CTA joins one head
 
 inline int head_rows(int group) { return group > 8 ? 16 : 8; }
 
@@ -49,13 +58,14 @@ struct BatchLayout {
 };
 
 // Workspace: int64 prefix[n_seqs + 1] (tiles of one unit of the sequences
-// before s), int64 CTA count; then slots [m, l, 0, 0, o[d]] of the unit's heads a piece.
+// before s), int64 warp count; then the group pieces and the end pieces, [m, l, 0, 0,
+// o[d]] for each of the unit's heads.
 inline BatchLayout batch_layout(const Geom& G, int32_t n_seqs) {
   BatchLayout b{};
   b.hu = head_rows(G.group);
   b.hb = (G.group + b.hu - 1) / b.hu;
   b.units = int64_t(n_seqs) * G.hkv * b.hb;
-  b.slots = kMaxCtas + b.units;
+  b.slots = 2 * kMaxWarps;
   b.slots_off = round_up((int64_t(n_seqs) + 2) * 8, 256);
   b.bytes = b.slots_off + round_up(b.slots * b.hu * (G.d + 4) * 4, 256);
   return b;
@@ -244,7 +254,7 @@ struct Queries<__nv_bfloat16, Qt, D, HU> {
             mma_bf16(s[n], a[st][0], 0u, a[st][1], 0u, kb[2 * u], kb[2 * u + 1]);
           } else {
             mma_bf16(s[n], a[st][0], a[st][1], a[st][2], a[st][3], kb[2 * u], kb[2 * u + 1]);
-            mma_bf16(s[n], 0u, b[st][0], 0u, b[st][1], kb[2 * u], kb[2 * u + 1]);
+            mma_bf16(low[n], 0u, b[st][0], 0u, b[st][1], kb[2 * u], kb[2 * u + 1]);
           }
         }
       }
@@ -255,8 +265,8 @@ struct Queries<__nv_bfloat16, Qt, D, HU> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
       } else {
-        s[n][0] += s[n][2];
-        s[n][1] += s[n][3];
+        s[n][0] += s[n][2] + low[n][2];
+        s[n][1] += s[n][3] + low[n][3];
       }
     }
   }
@@ -341,25 +351,26 @@ __device__ __forceinline__ void add_values(const __nv_bfloat16*, uint32_t tile, 
         for (int k = 0; k < TERMS; ++k) w[k][2 * half + r] = cut_bf16(p[2 * kb + half][2 * r], p[2 * kb + half][2 * r + 1]);
     const int row = kb * 16 + (lane & 15);
 #pragma unroll
-    for (int np = 0; np < D / 16; ++np) {
-      uint32_t v0, v1, v2, v3;
-      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3)
-                   : "r"(tile + Tile<__nv_bfloat16, D>::at_v(row, 2 * np + (lane >> 4)))
-                   : "memory");
+    for (int n0 = 0; n0 < D / 16; n0 += 4) {                 // 64 elements: every term in turn on 8 tiles of o
+      uint32_t v[8][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[2 * i][0]), "=r"(v[2 * i][1]), "=r"(v[2 * i + 1][0]), "=r"(v[2 * i + 1][1])
+                     : "r"(tile + Tile<__nv_bfloat16, D>::at_v(row, 2 * (n0 + i) + (lane >> 4)))
+                     : "memory");
       if constexpr (HU == 16) {
 #pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k) {
-          mma_bf16(o[2 * np], w[k][0], w[k][1], w[k][2], w[k][3], v0, v1);
-          mma_bf16(o[2 * np + 1], w[k][0], w[k][1], w[k][2], w[k][3], v2, v3);
-        }
+        for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mma_bf16(o[2 * n0 + i], w[k][0], w[k][1], w[k][2], w[k][3], v[i][0], v[i][1]);
       } else {
         if constexpr (TERMS == 3) {
-          mma_bf16(o[2 * np], 0u, w[2][0], 0u, w[2][2], v0, v1);
-          mma_bf16(o[2 * np + 1], 0u, w[2][0], 0u, w[2][2], v2, v3);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mma_bf16(o[2 * n0 + i], 0u, w[2][0], 0u, w[2][2], v[i][0], v[i][1]);
         }
-        mma_bf16(o[2 * np], w[0][0], w[1][0], w[0][2], w[1][2], v0, v1);
-        mma_bf16(o[2 * np + 1], w[0][0], w[1][0], w[0][2], w[1][2], v2, v3);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mma_bf16(o[2 * n0 + i], w[0][0], w[1][0], w[0][2], w[1][2], v[i][0], v[i][1]);
       }
     }
   }
@@ -403,20 +414,36 @@ __device__ __forceinline__ void add_values(const float*, uint32_t, const char* t
   }
 }
 
-// The head's element in column 2 t + e of o's n tile.
-template <typename Kv>
-__device__ __forceinline__ int element_of(int tile, int col) {
-  return sizeof(Kv) == 2 ? tile * 8 + col : (tile / 4) * 32 + col * 4 + tile % 4;
+__device__ __forceinline__ void put2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
 }
 
-template <int D>
-struct JoinSmem {
-  float o[kWarps][8][D];
-  float m[kWarps][8], l[kWarps][8];
+// Row r of o times f, lane t4's part of it. Column 2 t4 + e of o's tile i is the head's
+// element 8 i + 2 t4 + e (bf16 V) or 32 (i / 4) + 4 (2 t4 + e) + i % 4 (fp32 V).
+template <typename Kv, int D, typename Dst>
+__device__ __forceinline__ void put_row(Dst* row, int t4, int r, float f, const float (&o)[D / 8][4]) {
+#pragma unroll
+  for (int i = 0; i < D / 8; i += sizeof(Kv) == 2 ? 1 : 2) {
+    if constexpr (sizeof(Kv) == 2) {
+      put2(row + 8 * i + 2 * t4, o[i][2 * r] * f, o[i][2 * r + 1] * f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        put2(row + 32 * (i / 4) + 4 * (2 * t4 + e) + i % 4, o[i][2 * r + e] * f, o[i + 1][2 * r + e] * f);
+    }
+  }
+}
+
+struct BatchSmem {
   uint32_t mask[kWarps][kStages];                            // keys of a tile that are there
-  int64_t scan[kWarps], at[2];
+  int64_t scan[kWarps], at[kWarps][2];                       // where a warp's tiles begin: sequence, its first tile
+  int64_t unit[kWarps];                                      // the unit of a warp's open state, -1: none
+  int32_t starts[kWarps], ends[kWarps];                      // the warp has its first, its last tile
+  float m[kWarps][16], l[kWarps][16];
 };
-constexpr size_t batch_smem(int d) { return size_t(kWarps) * kStages * 2 * kTileBytes + (d == 128 ? sizeof(JoinSmem<128>) : sizeof(JoinSmem<64>)); }
+constexpr size_t kRingBytes = size_t(kWarps) * kStages * 2 * kTileBytes;
+constexpr size_t kBatchSmem = kRingBytes + sizeof(BatchSmem);
 
 template <typename Kv, typename Qt, int D, int HU>
 __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchArgs A) {
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
   constexpr int KEYS = T::kKeys, NT = KEYS / 8, NH = HU / 8;
   constexpr int TERMS = sizeof(Kv) == 4 || sizeof(Qt) == 2 ? 2 : 3;
   extern __shared__ __align__(128) char smem[];
-  JoinSmem<D>& J = *reinterpret_cast<JoinSmem<D>*>(smem + kWarps * kStages * 2 * kTileBytes);
+  BatchSmem& J = *reinterpret_cast<BatchSmem*>(smem + kRingBytes);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
   char* ring = smem + warp * kStages * 2 * kTileBytes;
   const uint32_t ring_at = uint32_t(__cvta_generic_to_shared(ring));
@@ -441,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
     if (tid == 0 && cur.ub == 0 && (n < 0 || n > A.max_tokens) && A.status != nullptr)
       atomicOr(A.status, ZHA_DEV_BAD_LENGTH);
     cur.n = clamped(A, cur.s);
-    cur.first = t0 = 0;
-    cur.end = t1 = tiles_of<KEYS>(cur.n);
+    cur.first = 0;
+    cur.end = tiles_of<KEYS>(cur.n);
     if (cur.n == 0) {
       const int h0 = (cur.ub % A.hb) * HU, heads = min(HU, A.group - h0);
       const int64_t qrow = int64_t(cur.s) * A.hq + int64_t(cur.ub / A.hb) * A.group + h0;
@@ -450,8 +477,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       if (tid < heads && A.lse != nullptr) A.lse[qrow + tid] = -INFINITY;
       return;
     }
+    const int n_w = int(min64(kWarps, cur.end));
+    t0 = warp < n_w ? warp * cur.end / n_w : cur.end;
+    t1 = warp < n_w ? (warp + 1) * cur.end / n_w : cur.end;
   } else {
-    // Tiles of all sequences and where this CTA's begin. Thread i scans a run of
+    // Tiles of all sequences and where this CTA's warps begin. Thread i scans a run of
     // ceil(S / threads) sequences.
     const int run = (A.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(A.n_seqs, tid * run), s1 = min(A.n_seqs, s0 + run);
@@ -472,33 +502,41 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       all += J.scan[w];
     }
     const int64_t total = all * per;
-    const int64_t c = blockIdx.x, n_cta = max64(1, min64(gridDim.x, (total + kWarps - 1) / kWarps));
-    t0 = c < n_cta ? c * total / n_cta : total;
-    t1 = c < n_cta ? (c + 1) * total / n_cta : total;
+    const int64_t n_w = max64(1, min64(int64_t(gridDim.x) * kWarps, (total + kMinTiles - 1) / kMinTiles));
+    const int64_t w0 = int64_t(blockIdx.x) * kWarps;
     for (int s = s0; s < s1; ++s) {
       const int64_t n = A.n_tokens[s], tl = tiles_of<KEYS>(clamped(A, s));
-      if (t0 >= at * per && t0 < (at + tl) * per) { J.at[0] = s; J.at[1] = at; }
-      if (c == 0) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int64_t t = w0 + w < n_w ? (w0 + w) * total / n_w : total;
+        if (t >= at * per && t < (at + tl) * per) { J.at[w][0] = s; J.at[w][1] = at; }
+      }
+      if (blockIdx.x == 0) {
         A.prefix[s] = at;
         if ((n < 0 || n > A.max_tokens) && A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_LENGTH);
       }
       at += tl;
     }
-    if (c == 0 && tid == 0) { A.prefix[A.n_seqs] = all; A.prefix[A.n_seqs + 1] = n_cta; }
+    if (blockIdx.x == 0 && tid == 0) { A.prefix[A.n_seqs] = all; A.prefix[A.n_seqs + 1] = n_w; }
     __syncthreads();
-    if (t0 >= t1) return;
-    cur.s = int(J.at[0]);
-    cur.n = clamped(A, cur.s);
-    const int64_t tl = tiles_of<KEYS>(cur.n), base = J.at[1] * per;
-    cur.ub = int((t0 - base) / tl);
-    cur.first = base + cur.ub * tl;
-    cur.end = cur.first + tl;
+    if (w0 >= n_w || total == 0) return;
+    const int64_t w = w0 + warp;
+    t0 = w < n_w ? w * total / n_w : total;
+    t1 = w < n_w ? (w + 1) * total / n_w : total;
+    if (t0 < t1) {
+      cur.s = int(J.at[warp][0]);
+      cur.n = clamped(A, cur.s);
+      const int64_t tl = tiles_of<KEYS>(cur.n), base = J.at[warp][1] * per;
+      cur.ub = int((t0 - base) / tl);
+      cur.first = base + cur.ub * tl;
+      cur.end = cur.first + tl;
+    }
   }
 
   // The ring. `row` is the cache row of the next tile's key `lane`, looked up one
   // tile ahead of its copy; -1: absent.
   Place ahead = cur;
-  int64_t next = t0 + warp;
+  int64_t next = t0;
   int32_t row = -1;
   auto look_up = [&] {
     row = -1;
@@ -523,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
         copy16(to + T::at_k(key, piece), static_cast<const char*>(A.kv.k) + off, r >= 0);
         copy16(to + kTileBytes + T::at_v(key, piece), static_cast<const char*>(A.kv.v) + off, r >= 0);
       }
-      next += kWarps;
+      ++next;
       look_up();
     }
     copy_commit();
@@ -532,21 +570,22 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-  int64_t at = t0 + warp;
+  int64_t at = t0;
   int stage = 0;
-  while (true) {
+  float m[NH], l[NH], o[D / 8][4];
+  if (lane == 0) J.unit[warp] = -1;
+  while (at < t1) {
     const int h0 = (cur.ub % A.hb) * HU, heads = min(HU, A.group - h0);
     const int64_t qrow = int64_t(cur.s) * A.hq + int64_t(cur.ub / A.hb) * A.group + h0;
     Queries<Kv, Qt, D, HU> q;
     q.load(static_cast<const Qt*>(A.Q) + qrow * D, heads, lane);
-    float m[NH], l[NH], o[D / 8][4];
 #pragma unroll
     for (int r = 0; r < NH; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     const int64_t stop = min64(t1, cur.end);
-    for (; at < stop; at += kWarps) {
+    for (; at < stop; ++at) {
       __syncwarp();                                          // the stage that is refilled has been read by all lanes
       issue(stage == 0 ? kStages - 1 : stage - 1);
       copy_wait<kStages - 1>();
@@ -604,101 +643,167 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 
-    // The warps' states joined, in warp order.
-    const bool whole = t0 <= cur.first && cur.end <= t1;
-    const int64_t unit = int64_t(cur.s) * per + cur.ub;
 #pragma unroll
     for (int r = 0; r < NH; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      __syncthreads();
-      if (t4 == 0) { J.m[warp][g] = m[r]; J.l[warp][g] = l[r]; }
+    }
+    if constexpr (HU == 8) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < D / 8; ++i) { o[i][0] += o[i][2]; o[i][1] += o[i][3]; }
+    }
+    const bool starts = cur.first >= t0, ends = cur.end <= t1;
+    if (starts && ends) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          J.o[warp][g][element_of<Kv>(i, 2 * t4 + e)] = HU == 8 ? o[i][e] + o[i][2 + e] : o[i][2 * r + e];
-      __syncthreads();
-      const int mine = min(8, heads - 8 * r);
-      for (int i = tid; i < mine * D; i += kThreads) {
-        const int h = i / D, e = i % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, J.m[w][h]);
-        float L = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float lw = J.l[w][h], f = lw != 0.f ? ex2(J.m[w][h] - M) : 0.f;
-          L += lw * f;
-          acc += J.o[w][h][e] * f;
+      for (int r = 0; r < NH; ++r)
+        if (g + 8 * r < heads) {
+          const int64_t out = qrow + g + 8 * r;
+          const float f = l[r] == 0.f ? 0.f : 1.f / l[r];
+          put_row<Kv, D>(static_cast<Qt*>(A.O) + out * D, t4, r, f, o);
+          if (t4 == 0 && A.lse != nullptr) A.lse[out] = l[r] == 0.f ? -INFINITY : 0.69314718056f * (m[r] + log2f(l[r]));
         }
-        const int64_t out = qrow + 8 * r + h;
-        if (whole) {
-          store_o(static_cast<Qt*>(A.O) + out * D + e, L == 0.f ? 0.f : acc / L);
-          if (e == 0 && A.lse != nullptr) A.lse[out] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
-        } else {
-          float* slot = A.slots + ((blockIdx.x + unit) * HU + 8 * r + h) * (D + 4);
-          slot[4 + e] = acc;
-          if (e == 0) { slot[0] = M; slot[1] = L; }
-        }
+    } else if (cur.end < t1) {
+      float* piece = A.slots + (kMaxWarps + int64_t(blockIdx.x) * kWarps + warp) * HU * (D + 4);
+#pragma unroll
+      for (int r = 0; r < NH; ++r) {
+        float* slot = piece + (g + 8 * r) * (D + 4);
+        put_row<Kv, D>(slot + 4, t4, r, 1.f, o);
+        if (t4 == 0) { slot[0] = m[r]; slot[1] = l[r]; }
+      }
+    } else if (lane == 0) {
+      J.unit[warp] = int64_t(cur.s) * per + cur.ub;
+      J.starts[warp] = starts;
+      J.ends[warp] = ends;
+    }
+    if (at < t1) next_unit<KEYS>(A, cur);
+  }
+
+  // The open states, joined where neighbouring warps have the same unit. The rings
+  // are done with.
+  copy_wait<0>();
+  __syncthreads();
+  float* states = reinterpret_cast<float*>(smem);            // [warp][HU][D]
+  if (J.unit[warp] >= 0) {
+#pragma unroll
+    for (int r = 0; r < NH; ++r) {
+      put_row<Kv, D>(states + (warp * HU + g + 8 * r) * D, t4, r, 1.f, o);
+      if (t4 == 0) { J.m[warp][g + 8 * r] = m[r]; J.l[warp][g + 8 * r] = l[r]; }
+    }
+  }
+  __syncthreads();
+  for (int a = 0, b; a < kWarps; a = b) {
+    const int64_t unit = J.unit[a];
+    for (b = a + 1; b < kWarps && J.unit[b] == unit; ++b) {}
+    if (unit < 0) continue;
+    const bool whole = J.starts[a] && J.ends[b - 1];
+    const int64_t s = unit / per;
+    const int ub = int(unit - s * per), h0 = (ub % A.hb) * HU, heads = min(HU, A.group - h0);
+    const int64_t qrow = s * A.hq + int64_t(ub / A.hb) * A.group + h0;
+    for (int i = tid; i < heads * D; i += kThreads) {
+      const int h = i / D, e = i % D;
+      float M = -INFINITY, L = 0.f, acc = 0.f;
+      for (int w = a; w < b; ++w) M = fmaxf(M, J.m[w][h]);
+      for (int w = a; w < b; ++w) {
+        const float lw = J.l[w][h], f = lw != 0.f ? ex2(J.m[w][h] - M) : 0.f;
+        L += lw * f;
+        acc += states[(w * HU + h) * D + e] * f;
+      }
+      if (whole) {
+        store_o(static_cast<Qt*>(A.O) + (qrow + h) * D + e, L == 0.f ? 0.f : acc / L);
+        if (e == 0 && A.lse != nullptr) A.lse[qrow + h] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
+      } else {
+        float* slot = A.slots + ((int64_t(blockIdx.x) * kWarps + a) * HU + h) * (D + 4);
+        slot[4 + e] = acc;
+        if (e == 0) { slot[0] = M; slot[1] = L; }
       }
     }
-    if (cur.end >= t1) break;
-    next_unit<KEYS>(A, cur);
   }
-  copy_wait<0>();
 }
 
-// One warp per (sequence, query head): nothing to do for a unit that one CTA
-// finished; zeros for one without tiles; else its pieces joined in CTA order.
+// a / b for quotients below 2^31 and a below 2^53: a quotient in 64-bit floats, then
+// put right (the hardware has no 64-bit integer division).
+__device__ __forceinline__ int quotient(int64_t a, int64_t b) {
+  int64_t q = int64_t(double(a) / double(b));
+  const int64_t r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return int(q);
+}
+
+// A unit's pieces joined: nothing to do for a finished unit; zeros for one without
+// tiles. Grid (units, heads): one CTA a head, its pieces dealt to the warps (few
+// units, many pieces each). Grid (units, 1): one warp a head.
 template <typename Qt, int D, int HU>
-__global__ void __launch_bounds__(kThreads) attend_batch_join_kernel(const BatchArgs A) {
-  constexpr int EPL = D / 32;
-  const int lane = threadIdx.x % 32;
-  const int64_t row = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
+__global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const BatchArgs A) {
+  constexpr int EPL = D / 32, kJoinWarps = kJoinThreads / 32;
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const bool wide = gridDim.y > 1;
+  const int split = wide ? kJoinWarps : 1, part = wide ? warp : 0;
   pdl_trigger();
   pdl_wait();
-  if (row >= int64_t(A.n_seqs) * A.hq) return;
-  const int s = int(row / A.hq), qh = int(row % A.hq), g = qh / A.group, hh = qh % A.group;
-  const int64_t per = int64_t(A.hkv) * A.hb, ub = int64_t(g) * A.hb + hh / HU;
+  const int per = A.hkv * A.hb, s = blockIdx.x / per, ub = blockIdx.x - s * per;
+  const int heads = min(HU, A.group - (ub % A.hb) * HU);
+  const int64_t row0 = int64_t(s) * A.hq + int64_t(ub / A.hb) * A.group + (ub % A.hb) * HU;
   const int64_t seq_tile = A.prefix[s], tl = A.prefix[s + 1] - seq_tile;
-  const int64_t total = A.prefix[A.n_seqs] * per, n_cta = A.prefix[A.n_seqs + 1];
-  float acc[EPL] = {}, M = -INFINITY, L = 0.f;
+  const int64_t total = A.prefix[A.n_seqs] * per, n_w = A.prefix[A.n_seqs + 1];
+  int w0 = 0, w1 = 0, groups = 0, n = 0;
   if (tl > 0) {
+    // Warps w0..w1 have the unit; the last one's state is an end piece unless the unit
+    // ends with that warp's tiles.
     const int64_t lo = seq_tile * per + ub * tl, hi = lo + tl;
-    const int64_t c0 = ((lo + 1) * n_cta - 1) / total;
-    const int n = int((hi * n_cta - 1) / total - c0) + 1;
-    if (n == 1) return;
-    const float* slots = A.slots + ((c0 + s * per + ub) * HU + hh % HU) * (D + 4);
-    constexpr int64_t step = int64_t(HU) * (D + 4);
-    for (int i = lane; i < n; i += 32)
-      if (slots[i * step + 1] != 0.f) M = fmaxf(M, slots[i * step]);
+    w0 = quotient((lo + 1) * n_w - 1, total);
+    w1 = quotient(hi * n_w - 1, total);
+    const bool apart = hi != quotient((w1 + 1) * total, n_w);
+    groups = w1 - apart < w0 ? 0 : (w1 - apart) / kWarps - w0 / kWarps + 1;
+    n = groups + apart;
+    if (w0 == w1 || n == 1) return;
+  }
+  for (int h = wide ? blockIdx.y : warp; h < heads; h += kJoinWarps) {
+    auto slot = [&](int i) {
+      const int64_t at = i < groups ? max(w0, (w0 / kWarps + i) * kWarps) : kMaxWarps + w1;
+      return const_cast<const float*>(A.slots) + (at * HU + h) * (D + 4);
+    };
+    float M = -INFINITY, L = 0.f, acc[EPL] = {};
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = __ldg(reinterpret_cast<const float2*>(slot(i)));
+      if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    }
     M = warp_max(M);
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float w = 0.f;
-      if (i0 + lane < n) {
-        const float l = slots[(i0 + lane) * step + 1];
-        if (l != 0.f) {
-          w = ex2(slots[(i0 + lane) * step] - M);
-          L += l * w;
-        }
-      }
-      const int most = min(32, n - i0);
 #pragma unroll 8
-      for (int i = 0; i < most; ++i) {
-        const float f = __shfl_sync(0xffffffffu, w, i);
-        float x[EPL];
-        load_slice<EPL>(slots + (i0 + i) * step + 4, lane * EPL, x);
+    for (int i = part; i < n; i += split) {
+      const float* p = slot(i);
+      const float2 ml = __ldg(reinterpret_cast<const float2*>(p));
+      float x[EPL];
+      load_slice<EPL>(p + 4, lane * EPL, x);
+      const float f = ml.y != 0.f ? ex2(ml.x - M) : 0.f;
+      L += ml.y * f;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = f == 0.f ? acc[e] : fmaf(x[e], f, acc[e]);
+      for (int e = 0; e < EPL; ++e) acc[e] = f == 0.f ? acc[e] : fmaf(x[e], f, acc[e]);
+    }
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
+      if (lane == 0) s_l[warp] = L;
+      __syncthreads();
+      if (warp != 0) return;
+      L = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinWarps; ++k) L += s_l[k];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        acc[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) acc[e] += s_o[k][lane * EPL + e];
       }
     }
-    L = warp_sum(L);
-  }
 #pragma unroll
-  for (int e = 0; e < EPL; ++e)
-    store_o(static_cast<Qt*>(A.O) + row * D + lane * EPL + e, L == 0.f ? 0.f : acc[e] / L);
-  if (lane == 0 && A.lse != nullptr) A.lse[row] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
+    for (int e = 0; e < EPL; ++e)
+      store_o(static_cast<Qt*>(A.O) + (row0 + h) * D + lane * EPL + e, L == 0.f ? 0.f : acc[e] / L);
+    if (lane == 0 && A.lse != nullptr) A.lse[row0 + h] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
+    if (wide) return;
+  }
 }
 
 template <typename Kv, typename Qt, int D, int HU>
@@ -707,24 +812,22 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   auto kernel = attend_batch_kernel<Kv, Qt, D, HU>;
-  e = ensure_dynamic_smem(kernel, batch_smem(D));
+  e = ensure_dynamic_smem(kernel, kBatchSmem);
   if (e != cudaSuccess) return e;
   const int64_t units = int64_t(A.n_seqs) * A.hkv * A.hb;
   const int64_t tiles = (A.max_tokens + Tile<Kv, D>::kKeys - 1) / Tile<Kv, D>::kKeys;
   A.single = tiles <= kSingleTiles && units <= int64_t(sms) * 2;
-  const int64_t ctas = A.single ? units : max64(1, min64(min64(int64_t(sms) * 2, kMaxCtas), (units * tiles + kWarps - 1) / kWarps));
+  const int64_t ctas = A.single ? units : max64(1, min64(min64(int64_t(sms) * 2, kMaxCtas), (units * tiles + kWarps * kMinTiles - 1) / (kWarps * kMinTiles)));
   {
     TraceScope ts("attend_batch_kernel", 0, s);
     zha_count_launch();
-    e = launch_pdl(kernel, dim3(unsigned(ctas)), dim3(kThreads), batch_smem(D), s, A);
+    e = launch_pdl(kernel, dim3(unsigned(ctas)), dim3(kThreads), kBatchSmem, s, A);
     if (e != cudaSuccess) return e;
   }
   if (A.single) return cudaSuccess;
   TraceScope ts("attend_batch_join_kernel", 0, s);
   zha_count_launch();
-  const int64_t rows = int64_t(A.n_seqs) * A.hq;
-  return launch_pdl(attend_batch_join_kernel<Qt, D, HU>, dim3(unsigned((rows + kWarps - 1) / kWarps)), dim3(kThreads), 0,
-                    s, A);
+  return launch_pdl(attend_batch_join_kernel<Qt, D, HU>, dim3(unsigned(units), unsigned(units <= kWideUnits ? min64(HU, A.group) : 1)), dim3(kJoinThreads), 0, s, A);
 }
 
 template <typename Kv, typename Qt>
