@@ -2,6 +2,7 @@
 // zha_host.cuh). Every entry is written once under a mutex and read afterwards.
 #include <mutex>
 #include <unordered_map>
+#include <unordered_set>
 
 #include "zha_host.cuh"
 
@@ -13,6 +14,7 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices] = {};
 std::unordered_map<const void*, size_t> g_smem[kMaxDevices];
+std::unordered_set<const void*> g_wide[kMaxDevices];
 
 }  // namespace
 
@@ -69,6 +71,19 @@ cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
                                 int(cudaSharedmemCarveoutMaxShared))) != cudaSuccess)
     return e;
   g_smem[dev][kernel] = bytes;
+  return cudaSuccess;
+}
+
+cudaError_t ensure_wide_cluster(const void* kernel) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices)
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (g_wide[dev].count(kernel)) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+  g_wide[dev].insert(kernel);
   return cudaSuccess;
 }
 

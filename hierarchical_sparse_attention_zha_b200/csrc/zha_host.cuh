@@ -28,4 +28,7 @@ inline cudaError_t ensure_dynamic_smem(void (*kernel)(Args...), size_t bytes) {
   return ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes);
 }
 
+// Clusters of more than 8 CTAs for `kernel` on the current device.
+cudaError_t ensure_wide_cluster(const void* kernel);
+
 }  // namespace zha

@@ -3,13 +3,16 @@
 //
 // The free pages are those with reference count 0, and the r-th page a call needs
 // (items, then KV heads, then blocks in order) is the r-th lowest free one. Both
-// ranks are prefix sums, so that no atomic's order shows in a result. Three launches:
-//   count  blocks of 2048 counts: how many are free (in use, for compact);
-//          one block per (item, KV head): is it valid, how many pages does it need
-//   list   each block's prefix over the blocks before it turns its free pages into
-//          list[rank]; one more block turns the needs into offsets
-//   fill   entries, counts and the rows to copy, with every rank known
-// Bound: the launches for small pools; the copied rows (HBM) for compact.
+// ranks are prefix sums, so that no atomic's order shows in a result. They want a few
+// passes over the counts with all of a pass done before the next, so one cluster of
+// up to 16 CTAs does them in one launch, with a cluster barrier between passes:
+//   1  how many pages are free (in use, for compact) in each CTA's share of the counts
+//   2  the shares' prefix turns every free page into list[rank]
+//   3  each (item, KV head): is it valid, how many pages does it need
+//   4  the needs' prefix, then entries and counts, with every rank known
+// What moves page contents is wide: a second launch over the whole GPU, unless it is
+// small enough to be done by the cluster.
+// Bound: the launch and the passes' latencies; the copied rows (HBM) for compact.
 #include <cstdio>
 
 #include "zha_host.cuh"
@@ -19,9 +22,12 @@ namespace zha {
 
 namespace {
 
-constexpr int kPageThreads = 256;
-constexpr int kSegment = 2048;            // reference counts per block
-constexpr int kPerThread = kSegment / kPageThreads;
+constexpr int kPageThreads = 256;         // of the kernels over the whole GPU
+constexpr int kBookThreads = 1024;        // of the cluster's CTAs
+constexpr int kBookWarps = kBookThreads / 32;
+constexpr int kPerThread = 4;             // counts a thread ranks in one go
+constexpr int kMostCtas = 16;
+constexpr int64_t kCopyHere = 256 << 10;  // bytes the cluster copies itself
 
 struct PoolArgs {
   char* k;
@@ -33,50 +39,52 @@ struct PoolArgs {
   int32_t* status;
 };
 
-// Workspace, int32: scal[8] (total free or live, total need, moves), seg[n_seg],
-// need[items * hkv], offs[items * hkv], list[n_pages], code[n_pages] (compact).
+// Workspace, int32: scal[8] (total free or live, moves), seg[16], first[n_seqs]
+// (the first item that lists a sequence), need, offs and copy[items * hkv],
+// list[n_pages], code[n_pages] (compact).
 struct PageWs {
-  int32_t *scal, *seg, *need, *offs, *list, *code;
+  int32_t *scal, *seg, *first, *need, *offs, *copy, *list, *code;
   int64_t bytes;
 };
 
-PageWs page_ws(void* base, int64_t n_pages, int64_t rows) {
-  const int64_t n_seg = (n_pages + kSegment - 1) / kSegment;
+PageWs page_ws(void* base, int64_t n_pages, int64_t n_seqs, int64_t rows) {
   int32_t* p = static_cast<int32_t*>(base);
   PageWs w{};
   int64_t at = 0;
   auto take = [&](int64_t n) { int32_t* q = base == nullptr ? nullptr : p + at; at += round_up(n, 64); return q; };
   w.scal = take(8);
-  w.seg = take(n_seg);
+  w.seg = take(kMostCtas);
+  w.first = take(n_seqs);
   w.need = take(rows);
   w.offs = take(rows);
+  w.copy = take(rows);
   w.list = take(n_pages);
   w.code = take(n_pages);
   w.bytes = at * 4;
   return w;
 }
 
-enum { kFree = 0, kNeed = 1, kMoves = 2 };
+enum { kLive = 0, kMoves = 1 };
 
 __device__ __forceinline__ void flag(const PoolArgs& P, int bit) {
   if (P.status != nullptr) atomicOr(P.status, bit);
 }
 
-// Sum over the block; every thread gets it.
-__device__ int block_sum(int v, int* s_red) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) s_red[threadIdx.x / 32] = v;
-  __syncthreads();
-  int t = 0;
-#pragma unroll
-  for (int w = 0; w < kPageThreads / 32; ++w) t += s_red[w];
-  return t;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// All of the cluster's threads, with what they wrote to global memory. What another
+// CTA wrote is then read past L1 (__ldcg).
+__device__ __forceinline__ void cluster_sync() {
+  __threadfence();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Exclusive prefix of v over the block's threads, and the sum of all.
 template <typename I>
-__device__ I block_prefix(I v, I* s_red, I* sum = nullptr) {
+__device__ I block_prefix(I v, I* s_red, I* sum) {
   I x = v;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
@@ -87,84 +95,110 @@ __device__ I block_prefix(I v, I* s_red, I* sum = nullptr) {
   __syncthreads();
   if (lane == 31) s_red[warp] = x;
   __syncthreads();
-  I base = 0, all = 0;
-  for (int w = 0; w < kPageThreads / 32; ++w) {
-    if (w < warp) base += s_red[w];
-    all += s_red[w];
+  I w = s_red[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  if (sum != nullptr) *sum = all;
-  return base + x - v;
+  *sum = __shfl_sync(0xffffffffu, w, kBookWarps - 1);
+  return (warp == 0 ? I(0) : __shfl_sync(0xffffffffu, w, warp - 1)) + x - v;
 }
 
 __device__ __forceinline__ bool counted(int32_t refs, bool live) { return live ? refs > 0 : refs == 0; }
 
-__device__ void count_segment(const PoolArgs& P, const PageWs& W, bool live, int* s_red) {
-  const int64_t base = int64_t(blockIdx.x) * kSegment;
-  int n = 0;
+struct Share {
+  int64_t p0, p1;
+};
+__device__ __forceinline__ Share share_of(int64_t n) {
+  return {int64_t(cluster_rank()) * n / gridDim.x, (int64_t(cluster_rank()) + 1) * n / gridDim.x};
+}
+
+// Pass 1: this CTA's share of the counts.
+__device__ void count_share(const PoolArgs& P, const PageWs& W, bool live, int* s_red) {
+  const Share h = share_of(P.n_pages);
+  int n = 0, sum;
+#pragma unroll 4
+  for (int64_t p = h.p0 + threadIdx.x; p < h.p1; p += kBookThreads) n += counted(P.refs[p], live);
+  block_prefix(n, s_red, &sum);
+  if (threadIdx.x == 0) W.seg[cluster_rank()] = sum;
+}
+
+// Pass 2: f(page, counted, exclusive rank) for the share's pages; returns the total.
+template <typename F>
+__device__ int rank_share(const PoolArgs& P, const PageWs& W, bool live, int* s_red, F f) {
+  const Share h = share_of(P.n_pages);
+  int base = 0, total = 0;
+  for (int i = 0; i < int(gridDim.x); ++i) {
+    const int v = __ldcg(W.seg + i);
+    if (i < int(cluster_rank())) base += v;
+    total += v;
+  }
+  for (int64_t q = h.p0; q < h.p1; q += kBookThreads * kPerThread) {
+    const int64_t p = q + threadIdx.x * kPerThread;
+    int n = 0, sum;
+    uint32_t bits = 0;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t p = base + i * kPageThreads + threadIdx.x;
-    if (p < P.n_pages) n += counted(P.refs[p], live);
+    for (int i = 0; i < kPerThread; ++i)
+      if (p + i < h.p1 && counted(P.refs[p + i], live)) { bits |= 1u << i; ++n; }
+    int rank = base + block_prefix(n, s_red, &sum);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (p + i >= h.p1) break;
+      const bool c = (bits >> i) & 1u;
+      f(p + i, c, rank);
+      rank += c;
+    }
+    base += sum;
   }
-  n = block_sum(n, s_red);
-  if (threadIdx.x == 0) W.seg[blockIdx.x] = n;
+  return total;
 }
 
-// ---- count -----------------------------------------------------------------
-__global__ void __launch_bounds__(kPageThreads) pages_count_live_kernel(PoolArgs P, PageWs W) {
-  __shared__ int s_red[kPageThreads / 32];
-  pdl_trigger();
-  pdl_wait();
-  count_segment(P, W, true, s_red);
+__device__ __forceinline__ void copy_bytes(char* to, const char* from, int64_t n, int id, int step) {
+  const uint4* f = reinterpret_cast<const uint4*>(from);
+  uint4* t = reinterpret_cast<uint4*>(to);
+#pragma unroll 4
+  for (int64_t i = id; i < n / 16; i += step) t[i] = f[i];
+}
+__device__ __forceinline__ void copy_rows(const PoolArgs& P, int32_t to, int32_t from, int64_t rows, int id, int step) {
+  const int64_t f = int64_t(from) * P.chunk * P.row_bytes, t = int64_t(to) * P.chunk * P.row_bytes;
+  copy_bytes(P.k + t, P.k + f, rows * P.row_bytes, id, step);
+  copy_bytes(P.v + t, P.v + f, rows * P.row_bytes, id, step);
 }
 
-// Whether `seq` stands in list[0, n).
-__device__ bool listed(const int32_t* list, int n, int32_t seq, int* s_red) {
-  int hit = 0;
-  for (int j = threadIdx.x; j < n; j += kPageThreads) hit |= list[j] == seq;
-  return block_sum(hit, s_red) != 0;
-}
-
-// kFork: src, dst, tokens; else seqs = dst.
+// ---- extend and fork ----------------------------------------------------------
+// Pass 3, one warp: how many pages row (item, head) needs, -1: refused.
 template <bool kFork>
-__global__ void __launch_bounds__(kPageThreads)
-    pages_count_kernel(PoolArgs P, PageWs W, int n_seg, const int32_t* src, const int32_t* dst, const int64_t* tokens,
-                       int n_items) {
-  __shared__ int s_red[kPageThreads / 32];
-  pdl_trigger();
-  pdl_wait();
-  if (int(blockIdx.x) < n_seg) {
-    count_segment(P, W, false, s_red);
-    return;
-  }
-  const int idx = blockIdx.x - n_seg, item = idx / P.hkv, g = idx % P.hkv;
-  const int32_t d = dst[item];
+__device__ int row_need(const PoolArgs& P, const PageWs& W, const int32_t* src, const int32_t* dst,
+                        const int64_t* tokens, int item, int g, int lane) {
+  const int32_t d = dst[item], s = kFork ? src[item] : d;
   const int64_t n = tokens[item];
   int bad = 0;
-  if (d < 0 || d >= P.n_seqs || listed(dst, item, d, s_red)) bad = ZHA_DEV_BAD_SEQUENCE;
-  int32_t s = d;
-  if (kFork) {
-    s = src[item];
-    if (s < 0 || s >= P.n_seqs || listed(dst, n_items, s, s_red)) bad = ZHA_DEV_BAD_SEQUENCE;
-  }
-  if (bad == 0 && (n < 0 || n > P.max_blocks * P.chunk)) bad = ZHA_DEV_BAD_LENGTH;
+  if (d < 0 || d >= P.n_seqs || s < 0 || s >= P.n_seqs) bad = ZHA_DEV_BAD_SEQUENCE;
+  else if (__ldcg(W.first + d) != item || (kFork && __ldcg(W.first + s) != INT32_MAX)) bad = ZHA_DEV_BAD_SEQUENCE;
+  else if (n < 0 || n > P.max_blocks * P.chunk) bad = ZHA_DEV_BAD_LENGTH;
   int need = 0;
   if (bad == 0) {
     const int64_t blocks = (n + P.chunk - 1) / P.chunk;
     const int32_t* row = P.table + (int64_t(s) * P.hkv + g) * P.max_blocks;
-    int miss = 0, wrong = 0;
-    for (int64_t b = threadIdx.x; b < blocks; b += kPageThreads) {
+    int miss = 0;
+    bool wrong = false, full = false;
+#pragma unroll 4
+    for (int64_t b = lane; b < blocks; b += 32) {
       const int32_t e = row[b];
       miss += e < 0;
       wrong |= e >= P.n_pages || (e >= 0 && P.refs[e] <= 0);
     }
-    miss = block_sum(miss, s_red);
-    wrong = block_sum(wrong, s_red);
     if (kFork) {
-      int full = 0;
       const int32_t* to = P.table + (int64_t(d) * P.hkv + g) * P.max_blocks;
-      for (int64_t b = threadIdx.x; b < P.max_blocks; b += kPageThreads) full |= to[b] >= 0;
-      if (block_sum(full, s_red)) bad = ZHA_DEV_BAD_SEQUENCE;
+#pragma unroll 4
+      for (int64_t b = lane; b < P.max_blocks; b += 32) full |= to[b] >= 0;
+    }
+    miss = __reduce_add_sync(0xffffffffu, miss);
+    wrong = __any_sync(0xffffffffu, wrong);
+    full = __any_sync(0xffffffffu, full);
+    if (kFork) {
+      if (full) bad = ZHA_DEV_BAD_SEQUENCE;
       else if (wrong || miss) bad = ZHA_DEV_BAD_PAGE;
       need = n % P.chunk != 0;
     } else {
@@ -172,138 +206,122 @@ __global__ void __launch_bounds__(kPageThreads)
       need = miss;
     }
   }
-  if (threadIdx.x == 0) {
-    W.need[idx] = bad ? -1 : need;
-    if (bad) flag(P, bad);
-  }
+  if (bad && lane == 0) flag(P, bad);
+  return bad ? -1 : need;
 }
 
-// ---- list ------------------------------------------------------------------
-// Exclusive prefix of this block's segment over the segments' counts, and (all
-// segments) the total.
-__device__ int segment_base(const PageWs& W, int n_seg, int* total, int* s_red) {
-  int below = 0, all = 0;
-  for (int i = threadIdx.x; i < n_seg; i += kPageThreads) {
-    const int v = W.seg[i];
-    all += v;
-    if (i < int(blockIdx.x)) below += v;
-  }
-  *total = block_sum(all, s_red);
-  return block_sum(below, s_red);
-}
-
-// Calls f(page, counted, exclusive rank) for the block's pages in order.
-template <typename F>
-__device__ void rank_segment(const PoolArgs& P, bool live, int base, int* s_red, F f) {
-  const int64_t p0 = int64_t(blockIdx.x) * kSegment + int64_t(threadIdx.x) * kPerThread;
-  int n = 0;
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i)
-    if (p0 + i < P.n_pages && counted(P.refs[p0 + i], live)) { bits |= 1u << i; ++n; }
-  int rank = base + block_prefix(n, s_red);
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    if (p0 + i >= P.n_pages) break;
-    const bool c = (bits >> i) & 1u;
-    f(p0 + i, c, rank);
-    rank += c;
-  }
-}
-
-__global__ void __launch_bounds__(kPageThreads) pages_list_kernel(PoolArgs P, PageWs W, int n_seg, int n_items) {
-  __shared__ int s_red[kPageThreads / 32];
-  pdl_trigger();
-  pdl_wait();
-  if (int(blockIdx.x) < n_seg) {
-    int total;
-    const int base = segment_base(W, n_seg, &total, s_red);
-    rank_segment(P, false, base, s_red, [&](int64_t p, bool c, int rank) {
-      if (c) W.list[rank] = int32_t(p);
-    });
-    if (blockIdx.x == 0 && threadIdx.x == 0) W.scal[kFree] = total;
-    return;
-  }
-  // Offsets of the (item, head) needs. One refused head refuses the item: its
-  // offset is then -1 and it needs nothing.
-  // Sums may pass 31 bits where no pool could serve them: they are kept in 64
-  // and stored cut to 31, which is above every count of free pages.
-  __shared__ int64_t s_red64[kPageThreads / 32];
-  constexpr int64_t kMost = 0x7fffffff;
-  int64_t carry = 0;
-  const int64_t rows = int64_t(n_items) * P.hkv;
-  for (int64_t r0 = 0; r0 < rows; r0 += kPageThreads) {
-    const int64_t r = r0 + threadIdx.x;
-    int64_t v = 0, sum;
-    bool ok = false;
-    if (r < rows) {
-      ok = true;
-      const int64_t i0 = r / P.hkv * P.hkv;
-      for (int g = 0; g < P.hkv; ++g) ok = ok && W.need[i0 + g] >= 0;
-      v = ok ? W.need[r] : 0;
-    }
-    const int64_t pre = block_prefix(v, s_red64, &sum);
-    if (r < rows) W.offs[r] = ok ? int32_t(min64(carry + pre, kMost)) : -1;
-    carry += sum;
-  }
-  if (threadIdx.x == 0) W.scal[kNeed] = int32_t(min64(carry, kMost));
-}
-
-// ---- fill ------------------------------------------------------------------
-__device__ __forceinline__ void copy_bytes(char* to, const char* from, int64_t n) {
-  const uint4* f = reinterpret_cast<const uint4*>(from);
-  uint4* t = reinterpret_cast<uint4*>(to);
-  for (int64_t i = threadIdx.x; i < n / 16; i += kPageThreads) t[i] = f[i];
-}
-
+// Pass 4, one warp: the pages list[at], ... go to row (item, head).
 template <bool kFork>
-__global__ void __launch_bounds__(kPageThreads)
-    pages_fill_kernel(PoolArgs P, PageWs W, const int32_t* src, const int32_t* dst, const int64_t* tokens) {
-  __shared__ int s_red[kPageThreads / 32];
-  pdl_trigger();
-  pdl_wait();
-  if (W.scal[kNeed] > W.scal[kFree]) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) flag(P, ZHA_DEV_NO_PAGES);
-    return;
-  }
-  const int idx = blockIdx.x, item = idx / P.hkv, g = idx % P.hkv;
-  int at = W.offs[idx];
-  if (at < 0) return;
+__device__ void fill_row(const PoolArgs& P, const PageWs& W, const int32_t* src, const int32_t* dst,
+                         const int64_t* tokens, int64_t idx, int at, bool copy_here, int lane) {
+  const int item = int(idx / P.hkv), g = int(idx % P.hkv);
   const int64_t n = tokens[item];
   int32_t* row = P.table + (int64_t(dst[item]) * P.hkv + g) * P.max_blocks;
   if (!kFork) {
     const int64_t blocks = (n + P.chunk - 1) / P.chunk;
-    for (int64_t b0 = 0; b0 < blocks; b0 += kPageThreads) {
-      const int64_t b = b0 + threadIdx.x;
-      const int miss = b < blocks && row[b] < 0;
-      int sum;
-      const int pre = block_prefix(miss, s_red, &sum);
+#pragma unroll 2
+    for (int64_t b0 = 0; b0 < blocks; b0 += 32) {
+      const int64_t b = b0 + lane;
+      const bool miss = b < blocks && row[b] < 0;
+      const uint32_t all = __ballot_sync(0xffffffffu, miss);
       if (miss) {
-        const int32_t page = W.list[at + pre];
+        const int32_t page = __ldcg(W.list + at + __popc(all & ((1u << lane) - 1)));
         row[b] = page;
         P.refs[page] = 1;
       }
-      at += sum;
+      at += __popc(all);
     }
     return;
   }
   const int64_t full = n / P.chunk, rest = n % P.chunk;
   const int32_t* from = P.table + (int64_t(src[item]) * P.hkv + g) * P.max_blocks;
-  const int32_t page = rest ? W.list[at] : -1;
-  for (int64_t b = threadIdx.x; b < P.max_blocks; b += kPageThreads) {
-    int32_t e = b == full ? page : -1;
+  const int32_t page = rest ? __ldcg(W.list + at) : -1;
+#pragma unroll 2
+  for (int64_t b = lane; b < full + (rest != 0); b += 32) {
+    int32_t e = page;
     if (b < full) {
       e = from[b];
       atomicAdd(&P.refs[e], 1);
     }
     row[b] = e;
   }
-  if (rest) {
-    if (threadIdx.x == 0) P.refs[page] = 1;
-    const int64_t f = int64_t(from[full]) * P.chunk * P.row_bytes, t = int64_t(page) * P.chunk * P.row_bytes;
-    copy_bytes(P.k + t, P.k + f, rest * P.row_bytes);
-    copy_bytes(P.v + t, P.v + f, rest * P.row_bytes);
+  if (rest == 0) return;
+  if (lane == 0) P.refs[page] = 1;
+  if (copy_here) copy_rows(P, page, from[full], rest, lane, 32);
+  else if (lane == 0) W.copy[idx] = page;
+}
+
+template <bool kFork>
+__global__ void __launch_bounds__(kBookThreads)
+    pages_items_kernel(PoolArgs P, PageWs W, const int32_t* src, const int32_t* dst, const int64_t* tokens, int n_items,
+                       bool copy_here) {
+  __shared__ int s_red[kBookWarps];
+  __shared__ int64_t s_red64[kBookWarps];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int id = int(cluster_rank()) * kBookThreads + threadIdx.x, step = int(gridDim.x) * kBookThreads;
+  for (int i = id; i < P.n_seqs; i += step) W.first[i] = INT32_MAX;
+  count_share(P, W, false, s_red);
+  cluster_sync();
+  for (int i = id; i < n_items; i += step) {
+    const int32_t d = dst[i];
+    if (d >= 0 && d < P.n_seqs) atomicMin(W.first + d, i);
   }
+  const int have = rank_share(P, W, false, s_red, [&](int64_t p, bool c, int rank) {
+    if (c) W.list[rank] = int32_t(p);
+  });
+  cluster_sync();
+  const int64_t rows = int64_t(n_items) * P.hkv;
+  const Share mine = share_of(rows);
+  for (int64_t r = mine.p0 + warp; r < mine.p1; r += kBookWarps) {
+    const int need = row_need<kFork>(P, W, src, dst, tokens, int(r / P.hkv), int(r % P.hkv), lane);
+    if (lane == 0) {
+      W.need[r] = need;
+      if (kFork) W.copy[r] = -1;
+    }
+  }
+  cluster_sync();
+  // Every CTA ranks all needs and keeps its rows' offsets; a refused head refuses its
+  // item (offset -1). Sums may pass 31 bits where no pool could serve them: they are
+  // kept in 64, and an offset that does not fit belongs to a call that changes nothing.
+  int64_t carry = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kBookThreads) {
+    const int64_t r = r0 + threadIdx.x;
+    int64_t v = 0, sum;
+    bool ok = false;
+    if (r < rows) {
+      ok = true;
+      const int64_t i0 = r / P.hkv * P.hkv;
+      for (int g = 0; g < P.hkv; ++g) ok &= __ldcg(W.need + i0 + g) >= 0;
+      v = ok ? __ldcg(W.need + r) : 0;
+    }
+    const int64_t at = carry + block_prefix(v, s_red64, &sum);
+    if (r >= mine.p0 && r < mine.p1) W.offs[r] = ok ? int32_t(min64(at, INT32_MAX)) : -1;
+    carry += sum;
+  }
+  if (carry > have) {
+    if (id == 0) flag(P, ZHA_DEV_NO_PAGES);
+    return;
+  }
+  __syncthreads();
+  for (int64_t r = mine.p0 + warp; r < mine.p1; r += kBookWarps) {
+    const int at = W.offs[r];
+    if (at >= 0) fill_row<kFork>(P, W, src, dst, tokens, r, at, copy_here, lane);
+  }
+}
+
+// The part-filled pages of a fork, one CTA per row.
+__global__ void __launch_bounds__(kPageThreads)
+    pages_copy_kernel(PoolArgs P, PageWs W, const int32_t* src, const int64_t* tokens) {
+  pdl_trigger();
+  pdl_wait();
+  const int32_t to = W.copy[blockIdx.x];
+  if (to < 0) return;
+  const int item = blockIdx.x / P.hkv, g = blockIdx.x % P.hkv;
+  const int64_t n = tokens[item];
+  const int32_t from = P.table[(int64_t(src[item]) * P.hkv + g) * P.max_blocks + n / P.chunk];
+  copy_rows(P, to, from, n % P.chunk, threadIdx.x, kPageThreads);
 }
 
 // ---- free ------------------------------------------------------------------
@@ -338,13 +356,42 @@ __global__ void __launch_bounds__(kPageThreads)
 // -2 - r for one that moves, r = its rank among the moving pages from the end. list[k]
 // = the k-th hole below n; list[n_pages - 1 - r] = the moving page r. There are
 // as many holes as moves, at most n_pages / 2, so the two ends do not meet.
-__global__ void __launch_bounds__(kPageThreads) pages_moves_kernel(PoolArgs P, PageWs W, int n_seg) {
-  __shared__ int s_red[kPageThreads / 32];
+__device__ void move_pages(const PoolArgs& P, const PageWs& W, int32_t* page_map, int32_t* n_live) {
+  const int moves = __ldcg(W.scal + kMoves), threads = blockDim.x;
+  auto place = [&](int32_t code) { return code < -1 ? __ldcg(W.list + moves - 1 - (-2 - code)) : code; };
+  for (int k = blockIdx.x; k < moves; k += gridDim.x) {
+    const int32_t to = __ldcg(W.list + k), from = __ldcg(W.list + P.n_pages - 1 - (moves - 1 - k));
+    copy_rows(P, to, from, P.chunk, threadIdx.x, threads);
+    if (threadIdx.x == 0) {
+      P.refs[to] = P.refs[from];
+      P.refs[from] = 0;
+    }
+  }
+  const int64_t cells = int64_t(P.n_seqs) * P.hkv * P.max_blocks, step = int64_t(gridDim.x) * threads;
+  const int64_t id = int64_t(blockIdx.x) * threads + threadIdx.x;
+#pragma unroll 4
+  for (int64_t i = id; i < cells; i += step) {
+    const int32_t e = P.table[i];
+    if (e < 0 || e >= P.n_pages) continue;
+    const int32_t to = place(__ldcg(W.code + e));
+    if (to < 0) flag(P, ZHA_DEV_BAD_PAGE);
+    if (to != e) P.table[i] = to;
+  }
+  if (page_map != nullptr)
+    for (int64_t p = id; p < P.n_pages; p += step) page_map[p] = place(__ldcg(W.code + p));
+  if (n_live != nullptr && id == 0) *n_live = __ldcg(W.scal + kLive);
+}
+
+__global__ void __launch_bounds__(kBookThreads)
+    pages_plan_kernel(PoolArgs P, PageWs W, int32_t* page_map, int32_t* n_live, bool move_here) {
+  __shared__ int s_red[kBookWarps];
   pdl_trigger();
   pdl_wait();
-  int n;
-  const int base = segment_base(W, n_seg, &n, s_red);
-  rank_segment(P, true, base, s_red, [&](int64_t p, bool live, int rank) {
+  count_share(P, W, true, s_red);
+  cluster_sync();
+  int n = 0;
+  for (int i = 0; i < int(gridDim.x); ++i) n += __ldcg(W.seg + i);
+  rank_share(P, W, true, s_red, [&](int64_t p, bool live, int rank) {
     int32_t code = -1;
     if (live) {
       code = int32_t(p);
@@ -359,40 +406,20 @@ __global__ void __launch_bounds__(kPageThreads) pages_moves_kernel(PoolArgs P, P
     W.code[p] = code;
     if (p == n - 1) W.scal[kMoves] = n - rank - live;      // holes below n
   });
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    W.scal[kFree] = n;
+  if (cluster_rank() == 0 && threadIdx.x == 0) {
+    W.scal[kLive] = n;
     if (n == 0) W.scal[kMoves] = 0;
   }
+  if (!move_here) return;
+  cluster_sync();
+  move_pages(P, W, page_map, n_live);
 }
 
 __global__ void __launch_bounds__(kPageThreads)
     pages_move_kernel(PoolArgs P, PageWs W, int32_t* page_map, int32_t* n_live) {
   pdl_trigger();
   pdl_wait();
-  const int moves = W.scal[kMoves];
-  const int64_t page_bytes = int64_t(P.chunk) * P.row_bytes;
-  auto place = [&](int32_t code) { return code < -1 ? W.list[moves - 1 - (-2 - code)] : code; };
-  for (int k = blockIdx.x; k < moves; k += gridDim.x) {
-    const int32_t to = W.list[k], from = W.list[P.n_pages - 1 - (moves - 1 - k)];
-    copy_bytes(P.k + to * page_bytes, P.k + from * page_bytes, page_bytes);
-    copy_bytes(P.v + to * page_bytes, P.v + from * page_bytes, page_bytes);
-    if (threadIdx.x == 0) {
-      P.refs[to] = P.refs[from];
-      P.refs[from] = 0;
-    }
-  }
-  const int64_t cells = int64_t(P.n_seqs) * P.hkv * P.max_blocks, step = int64_t(gridDim.x) * kPageThreads;
-  const int64_t id = int64_t(blockIdx.x) * kPageThreads + threadIdx.x;
-  for (int64_t i = id; i < cells; i += step) {
-    const int32_t e = P.table[i];
-    if (e < 0 || e >= P.n_pages) continue;
-    const int32_t to = place(W.code[e]);
-    if (to < 0) flag(P, ZHA_DEV_BAD_PAGE);
-    if (to != e) P.table[i] = to;
-  }
-  if (page_map != nullptr)
-    for (int64_t p = id; p < P.n_pages; p += step) page_map[p] = place(W.code[p]);
-  if (n_live != nullptr && id == 0) *n_live = W.scal[kFree];
+  move_pages(P, W, page_map, n_live);
 }
 
 zha_status pool_args(const zha_config* cfg, const zha_page_pool* pool, const char* who, PoolArgs* out) {
@@ -432,8 +459,6 @@ zha_status pool_args(const zha_config* cfg, const zha_page_pool* pool, const cha
   return ZHA_OK;
 }
 
-int segments(const PoolArgs& P) { return int((P.n_pages + kSegment - 1) / kSegment); }
-
 zha_status need_ws(void* d_ws, size_t have, int64_t need) {
   if (d_ws != nullptr && reinterpret_cast<uintptr_t>(d_ws) % 256 == 0 && int64_t(have) >= need) return ZHA_OK;
   return zha_report_error(ZHA_ERR_CAPACITY, "zha_pages: workspace must be 256-byte aligned with zha_pages_workspace_bytes");
@@ -457,22 +482,45 @@ zha_status launch_page_kernel(const char* name, const char* who, void (*kernel)(
   return e == cudaSuccess ? ZHA_OK : zha_report_cuda(e, who);
 }
 
-// extend and fork: count, list, fill.
+// One cluster, of one CTA per 4096 counts or 32 rows.
+template <typename... K, typename... A>
+zha_status launch_book(const char* name, const char* who, void (*kernel)(K...), const PoolArgs& P, int64_t rows,
+                       cudaStream_t s, A&&... args) {
+  const int64_t want = max64((P.n_pages + 4095) / 4096, (rows + 31) / 32);
+  int ctas = 1;
+  while (ctas < want && ctas < kMostCtas) ctas *= 2;
+  cudaError_t e = ensure_wide_cluster(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return zha_report_cuda(e, who);
+  TraceScope ts(name, 0, s);
+  zha_count_launch();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kBookThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
+  return e == cudaSuccess ? ZHA_OK : zha_report_cuda(e, who);
+}
+
 template <bool kFork>
 zha_status run_items(const PoolArgs& P, const int32_t* src, const int32_t* dst, const int64_t* tokens, int32_t n_items,
                      void* d_ws, size_t ws_bytes, cudaStream_t s, const char* who) {
   const int64_t rows = int64_t(n_items) * P.hkv;
-  const PageWs W = page_ws(d_ws, P.n_pages, rows);
+  const PageWs W = page_ws(d_ws, P.n_pages, P.n_seqs, rows);
   zha_status st = need_ws(d_ws, ws_bytes, W.bytes);
   if (st != ZHA_OK) return st;
-  const int n_seg = segments(P);
-  if ((st = launch_page_kernel("pages_count_kernel", who, pages_count_kernel<kFork>, n_seg + rows, s, P, W, n_seg, src,
-                               dst, tokens, n_items)) != ZHA_OK)
-    return st;
-  if ((st = launch_page_kernel("pages_list_kernel", who, pages_list_kernel, n_seg + 1, s, P, W, n_seg, n_items)) !=
-      ZHA_OK)
-    return st;
-  return launch_page_kernel("pages_fill_kernel", who, pages_fill_kernel<kFork>, rows, s, P, W, src, dst, tokens);
+  const bool copy_here = rows * P.chunk * P.row_bytes <= kCopyHere;
+  st = launch_book("pages_items_kernel", who, pages_items_kernel<kFork>, P, rows, s, P, W, src, dst, tokens, n_items,
+                   copy_here);
+  if (st != ZHA_OK || !kFork || copy_here) return st;
+  return launch_page_kernel("pages_copy_kernel", who, pages_copy_kernel, rows, s, P, W, src, tokens);
 }
 
 }  // namespace
@@ -488,7 +536,7 @@ size_t zha_pages_workspace_bytes(const zha_config* cfg, const zha_page_pool* poo
   if (zha::pool_args(cfg, pool, "zha_pages_workspace_bytes", &P) != ZHA_OK || n_items < 0 || n_items > 65535 ||
       int64_t(n_items) * P.hkv > zha::kMaxItemRows)
     return 0;
-  return size_t(zha::page_ws(nullptr, P.n_pages, int64_t(n_items) * P.hkv).bytes);
+  return size_t(zha::page_ws(nullptr, P.n_pages, P.n_seqs, int64_t(n_items) * P.hkv).bytes);
 }
 
 zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_seqs,
@@ -537,17 +585,15 @@ zha_status zha_pages_compact(const zha_config* cfg, const zha_page_pool* pool, i
   zha_status st = zha::pool_args(cfg, pool, who, &P);
   if (st != ZHA_OK) return st;
   P.status = d_status;
-  const zha::PageWs W = zha::page_ws(d_ws, P.n_pages, 0);
+  const zha::PageWs W = zha::page_ws(d_ws, P.n_pages, P.n_seqs, 0);
   if ((st = zha::need_ws(d_ws, ws_bytes, W.bytes)) != ZHA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
   const cudaError_t e = zha::device_sm_count(&sms);
   if (e != cudaSuccess) return zha_report_cuda(e, who);
-  const int n_seg = zha::segments(P);
-  if ((st = zha::launch_page_kernel("pages_count_live_kernel", who, zha::pages_count_live_kernel, n_seg, s, P, W)) != ZHA_OK)
-    return st;
-  if ((st = zha::launch_page_kernel("pages_moves_kernel", who, zha::pages_moves_kernel, n_seg, s, P, W, n_seg)) != ZHA_OK)
-    return st;
+  const bool move_here = P.n_pages * P.chunk * P.row_bytes <= 2 * zha::kCopyHere;
+  st = zha::launch_book("pages_plan_kernel", who, zha::pages_plan_kernel, P, 0, s, P, W, d_page_map, d_n_live, move_here);
+  if (st != ZHA_OK || move_here) return st;
   return zha::launch_page_kernel("pages_move_kernel", who, zha::pages_move_kernel, int64_t(sms) * 8, s, P, W,
                                  d_page_map, d_n_live);
 }

@@ -448,27 +448,42 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _args(device, status, ws=None) -> None:
-    """The current device's tensors, a status word and a workspace."""
-    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
-          "tensors must lie on the current CUDA device")
-    _need(status is None or (status.dtype == torch.int32 and status.device == device),
-          "status must be an int32 tensor on the same device")
-    _need(ws is None or (ws.device == device and ws.is_contiguous()),
-          "ws must be a contiguous tensor on the same device")
+# (Each check is an `if` of its own: a small call's time on the host is what it costs.)
+
+def _run_on(device, stream) -> int:
+    """The stream of a call on tensors of `device`, which must be the current one."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("tensors must lie on the current CUDA device")
+    # (torch.cuda.current_stream() makes an object of it, which takes 3 us)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-def _int_list(x: torch.Tensor, dtype, n: int, device, name: str) -> int:
-    _need(x.dtype == dtype and x.device == device and x.shape == (n,) and x.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor [{n}] on the same device")
+def _status_ptr(status: torch.Tensor | None, device):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor on the same device")
+    return status.data_ptr()
+
+
+def _scratch(ws: torch.Tensor, device) -> tuple[int, int]:
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the same device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _list_ptr(x: torch.Tensor, dtype, n: int, device, name: str) -> int:
+    if x.dtype != dtype or x.device != device or x.shape != (n,) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] on the same device")
     return x.data_ptr()
 
 
 def _same_cache(cfg: Config, c) -> None:
     """A configuration and a kv_batch() or page_pool() that describe one cache."""
     s = c.shape
-    _need(c.heads == cfg.n_kv_heads and s[-1] == cfg.head_dim and c.dtype == cfg.kv_dtype
-          and (len(s) == 4 or s[1] == cfg.chunk), "the cache does not match the configuration")
+    if (c.heads != cfg.n_kv_heads or s[-1] != cfg.head_dim or c.dtype != cfg.kv_dtype
+            or (len(s) == 3 and s[1] != cfg.chunk)):
+        raise ValueError("the cache does not match the configuration")
 
 
 class Rope:
@@ -489,28 +504,30 @@ class Rope:
         check(lib.zha_rope_init(byref(spec), byref(self.table)), "zha_rope_init")
 
 
-def _rows(x: torch.Tensor, tokens: int, heads: int, d: int, device, name: str) -> Rows:
-    _need(x.shape == (tokens, heads, d) and x.device == device and (x.stride(2) == 1 or x.numel() == 0),
-          f"{name} must be [{tokens}, {heads}, {d}] with rows of adjacent elements, on the same device")
-    return Rows(x.data_ptr(), x.stride(0) if tokens > 1 else 0, x.stride(1) if heads > 1 else 0)
+def _rows(x: torch.Tensor, shape: tuple, device, name: str) -> Rows:
+    stride = x.stride()
+    if x.shape != shape or x.device != device or (stride[2] != 1 and x.numel() > 0):
+        raise ValueError(f"{name} must be {list(shape)} with rows of adjacent elements, on the same device")
+    return Rows(x.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
 def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | None = None,
                inverse: bool = False, stream=None) -> torch.Tensor:
     """zha_rope_apply: x [T, heads, d] (float32 or bf16, any token and head strides) turned
     at pos [T] int64, or turned back (the gradient's direction). `out` may be x."""
-    _need(x.dim() == 3 and x.dtype in _DTYPE, "x must be [T, heads, d], float32 or bfloat16")
-    T, H, d = x.shape
-    _need(d == rope.table.head_dim, "x does not match the rotation's head_dim")
-    dev = x.device
-    _args(dev, None)
+    shape, dev, dtype = x.shape, x.device, _DTYPE.get(x.dtype)
+    if len(shape) != 3 or dtype is None or shape[2] != rope.table.head_dim:
+        raise ValueError("x must be [T, heads, head_dim] of the rotation, float32 or bfloat16")
+    on = _run_on(dev, stream)
     if out is None:
-        out = torch.empty(T, H, d, dtype=x.dtype, device=dev)
-    _need(out.dtype in _DTYPE, "out must be float32 or bfloat16")
-    rx, ry = _rows(x, T, H, d, dev, "x"), _rows(out, T, H, d, dev, "out")
-    check(lib.zha_rope_apply(byref(rope.table), byref(rx), _DTYPE[x.dtype], _int_list(pos, torch.int64, T, dev, "pos"),
-                             T, H, 1 if inverse else 0, byref(ry), _DTYPE[out.dtype], stream_ptr(stream)),
-          "zha_rope_apply")
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    to = _DTYPE.get(out.dtype)
+    if to is None:
+        raise ValueError("out must be float32 or bfloat16")
+    rx = _rows(x, shape, dev, "x")
+    ry = rx if out is x else _rows(out, shape, dev, "out")
+    check(lib.zha_rope_apply(byref(rope.table), byref(rx), dtype, _list_ptr(pos, torch.int64, shape[0], dev, "pos"),
+                             shape[0], shape[1], 1 if inverse else 0, byref(ry), to, on), "zha_rope_apply")
     return out
 
 
@@ -522,26 +539,31 @@ def rope_append_kv(cfg: Config, rope: Rope | None, q: torch.Tensor | None, k: to
     sequence seq[t], keys turned at pos (None: index); q [T, Hq, d] turned into q_out, which
     is returned (None without q). rope None: nothing is turned."""
     _same_cache(cfg, kv)
-    _need(1 <= n_seqs <= kv.seqs, "n_seqs is more than the caches hold")
-    T, H, Hq, d = k.shape[0], cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
-    dev = kv.device
-    _args(dev, status)
-    _need(k.dtype in _DTYPE and v.dtype == k.dtype and (q is None or q.dtype == k.dtype),
-          "q, k and v must have one type, float32 or bfloat16")
-    rk, rv = _rows(k, T, H, d, dev, "k"), _rows(v, T, H, d, dev, "v")
-    rq = None
+    if not 1 <= n_seqs <= kv.seqs:
+        raise ValueError("n_seqs is more than the caches hold")
+    H, Hq, d = cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
+    T, dev, dtype = k.shape[0], kv.device, _DTYPE.get(k.dtype)
+    on = _run_on(dev, stream)
+    if dtype is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k and v must have one type, float32 or bfloat16")
+    shape = (T, H, d)
+    rk, rv = _rows(k, shape, dev, "k"), _rows(v, shape, dev, "v")
+    rq = to = None
+    q_type = ZHA_F32
     if q is not None:
-        rq = _rows(q, T, Hq, d, dev, "q")
+        shape = (T, Hq, d)
+        rq = byref(_rows(q, shape, dev, "q"))
         if q_out is None:
-            q_out = torch.empty(T, Hq, d, dtype=q_dtype, device=dev)
-        _need(q_out.shape == (T, Hq, d) and q_out.is_contiguous() and q_out.device == dev and q_out.dtype in _DTYPE,
-              f"q_out must be a contiguous float32 or bfloat16 tensor [{T}, {Hq}, {d}]")
+            q_out = torch.empty(shape, dtype=q_dtype, device=dev)
+        q_type = _DTYPE.get(q_out.dtype)
+        if q_type is None or q_out.shape != shape or q_out.device != dev or not q_out.is_contiguous():
+            raise ValueError(f"q_out must be a contiguous float32 or bfloat16 tensor {list(shape)}")
+        to = q_out.data_ptr()
     check(lib.zha_rope_append_kv(
-        byref(cfg), None if rope is None else byref(rope.table), None if rq is None else byref(rq), byref(rk), byref(rv),
-        _DTYPE[k.dtype], T, byref(kv), n_seqs, _int_list(seq, torch.int32, T, dev, "seq"),
-        _int_list(index, torch.int64, T, dev, "index"), None if pos is None else _int_list(pos, torch.int64, T, dev, "pos"),
-        None if q is None else q_out.data_ptr(), ZHA_F32 if q is None else _DTYPE[q_out.dtype],
-        ptr(status), stream_ptr(stream)), "zha_rope_append_kv")
+        byref(cfg), None if rope is None else byref(rope.table), rq, byref(rk), byref(rv), dtype, T, byref(kv), n_seqs,
+        _list_ptr(seq, torch.int32, T, dev, "seq"), _list_ptr(index, torch.int64, T, dev, "index"),
+        None if pos is None else _list_ptr(pos, torch.int64, T, dev, "pos"), to, q_type, _status_ptr(status, dev), on),
+        "zha_rope_append_kv")
     return None if q is None else q_out
 
 
@@ -555,35 +577,37 @@ def attend_batch_kv(cfg: Config, Q: torch.Tensor, kv: KvCache, n_seqs: int, n_to
     """zha_attend_batch_kv: Q [n_seqs, Hq, d] (float32 or bf16) over the first n_tokens [n_seqs]
     (int64) tokens of each cache of kv_batch(); (out, lse), out of Q's type."""
     _same_cache(cfg, kv)
-    _need(1 <= n_seqs <= kv.seqs, "n_seqs is more than the caches hold")
-    dev = kv.device
+    if not 1 <= n_seqs <= kv.seqs:
+        raise ValueError("n_seqs is more than the caches hold")
+    dev, dtype = kv.device, _DTYPE.get(Q.dtype)
+    on = _run_on(dev, stream)
     want = (n_seqs, cfg.n_q_heads, cfg.head_dim)
-    _need(Q.shape == want and Q.dtype in _DTYPE and Q.is_contiguous() and Q.device == dev,
-          f"Q must be a contiguous float32 or bfloat16 tensor {list(want)} on the cache's device")
+    if dtype is None or Q.shape != want or Q.device != dev or not Q.is_contiguous():
+        raise ValueError(f"Q must be a contiguous float32 or bfloat16 tensor {list(want)} on the cache's device")
     if out is None:
         out = torch.empty_like(Q)
+    elif out.shape != want or out.dtype != Q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of Q's shape and type")
     if lse is None:
         lse = torch.empty(want[:2], dtype=torch.float32, device=dev)
+    elif lse.shape != want[:2] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [n_seqs, Hq]")
     if ws is None:
         ws = _bytes_tensor(attend_batch_workspace_bytes(cfg, n_seqs, max_tokens), dev)
-    _args(dev, status, ws)
-    _need(out.shape == want and out.dtype == Q.dtype and out.is_contiguous() and out.device == dev,
-          "out must be a contiguous tensor of Q's shape and type")
-    _need(lse.shape == want[:2] and lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev,
-          "lse must be a contiguous float32 tensor [n_seqs, Hq]")
-    check(lib.zha_attend_batch_kv(byref(cfg), Q.data_ptr(), _DTYPE[Q.dtype], byref(kv), n_seqs,
-                                  _int_list(n_tokens, torch.int64, n_seqs, dev, "n_tokens"), max_tokens,
-                                  out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                  ptr(status), stream_ptr(stream)), "zha_attend_batch_kv")
+    check(lib.zha_attend_batch_kv(byref(cfg), Q.data_ptr(), dtype, byref(kv), n_seqs,
+                                  _list_ptr(n_tokens, torch.int64, n_seqs, dev, "n_tokens"), max_tokens, out.data_ptr(),
+                                  lse.data_ptr(), *_scratch(ws, dev), _status_ptr(status, dev), on),
+          "zha_attend_batch_kv")
     return out, lse
 
 
 def page_pool(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor, refs: torch.Tensor) -> PagePool:
     """A zha_page_pool over K, V [n_pages, C, d], block_table [n_seqs, Hkv, max_blocks] and refs
     [n_pages] (both int32). It keeps the tensors alive."""
+    _need(block_table is not None, "a page pool needs a block table")
     kv = kv_batch(K, V, block_table)
-    _int_list(refs, torch.int32, K.shape[0], K.device, "refs")
-    p = PagePool(kv.k, kv.v, kv.ld, kv.block_table, kv.max_blocks, refs.data_ptr(), block_table.shape[0], 0)
+    p = PagePool(kv.k, kv.v, kv.ld, kv.block_table, kv.max_blocks,
+                 _list_ptr(refs, torch.int32, K.shape[0], K.device, "refs"), block_table.shape[0], 0)
     p.tensors = (*kv.tensors, refs)
     p.shape, p.dtype, p.heads, p.seqs, p.device = kv.shape, kv.dtype, kv.heads, kv.seqs, kv.device
     return p
@@ -593,55 +617,56 @@ def pages_workspace_bytes(cfg: Config, pool: PagePool, n_items: int) -> int:
     return int(lib.zha_pages_workspace_bytes(byref(cfg), byref(pool), n_items))
 
 
-def _pages(cfg, pool, n_items, ws, status, need_ws=True):
-    _same_cache(cfg, pool)
-    if ws is None and need_ws:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n_items), pool.device)
-    _args(pool.device, status, ws)
-    return ws
-
-
 def pages_extend(cfg: Config, pool: PagePool, seqs: torch.Tensor, n_tokens: torch.Tensor,
                  ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_extend: pages for the first n_tokens[i] (int64) tokens of sequence seqs[i] (int32)."""
-    n = seqs.numel()
-    ws = _pages(cfg, pool, n, ws, status)
-    check(lib.zha_pages_extend(byref(cfg), byref(pool), _int_list(seqs, torch.int32, n, pool.device, "seqs"),
-                               _int_list(n_tokens, torch.int64, n, pool.device, "n_tokens"), n, ws.data_ptr(),
-                               ws.numel() * ws.element_size(), ptr(status), stream_ptr(stream)), "zha_pages_extend")
+    _same_cache(cfg, pool)
+    n, dev = seqs.numel(), pool.device
+    on = _run_on(dev, stream)
+    if ws is None:
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), dev)
+    check(lib.zha_pages_extend(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
+                               _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
+                               _status_ptr(status, dev), on), "zha_pages_extend")
 
 
 def pages_fork(cfg: Config, pool: PagePool, src: torch.Tensor, dst: torch.Tensor, n_tokens: torch.Tensor,
                ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_fork: the empty sequence dst[i] becomes the first n_tokens[i] tokens of src[i]."""
-    n = dst.numel()
-    ws = _pages(cfg, pool, n, ws, status)
-    dev = pool.device
-    check(lib.zha_pages_fork(byref(cfg), byref(pool), _int_list(src, torch.int32, n, dev, "src"),
-                             _int_list(dst, torch.int32, n, dev, "dst"),
-                             _int_list(n_tokens, torch.int64, n, dev, "n_tokens"), n, ws.data_ptr(),
-                             ws.numel() * ws.element_size(), ptr(status), stream_ptr(stream)), "zha_pages_fork")
+    _same_cache(cfg, pool)
+    n, dev = dst.numel(), pool.device
+    on = _run_on(dev, stream)
+    if ws is None:
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), dev)
+    check(lib.zha_pages_fork(byref(cfg), byref(pool), _list_ptr(src, torch.int32, n, dev, "src"),
+                             _list_ptr(dst, torch.int32, n, dev, "dst"),
+                             _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
+                             _status_ptr(status, dev), on), "zha_pages_fork")
 
 
 def pages_free(cfg: Config, pool: PagePool, seqs: torch.Tensor, keep: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_free: sequences seqs [n] give up their pages behind the first keep [n] (int64)
     tokens (None: all). Needs no workspace; ws is taken for symmetry and not used."""
-    n = seqs.numel()
-    _pages(cfg, pool, n, ws, status, need_ws=False)
-    check(lib.zha_pages_free(byref(cfg), byref(pool), _int_list(seqs, torch.int32, n, pool.device, "seqs"),
-                             None if keep is None else _int_list(keep, torch.int64, n, pool.device, "keep"), n,
-                             ptr(status), stream_ptr(stream)), "zha_pages_free")
+    _same_cache(cfg, pool)
+    n, dev = seqs.numel(), pool.device
+    on = _run_on(dev, stream)
+    check(lib.zha_pages_free(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
+                             None if keep is None else _list_ptr(keep, torch.int64, n, dev, "keep"), n,
+                             _status_ptr(status, dev), on), "zha_pages_free")
 
 
 def pages_compact(cfg: Config, pool: PagePool, page_map: torch.Tensor | None = None, n_live: torch.Tensor | None = None,
                   ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_compact: the pages in use become [0, n); page_map [n_pages] and n_live [1]
     (int32, both may be None) say where each went and how many they are."""
-    ws = _pages(cfg, pool, 0, ws, status)
+    _same_cache(cfg, pool)
     dev = pool.device
+    on = _run_on(dev, stream)
+    if ws is None:
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, 0), dev)
     check(lib.zha_pages_compact(
         byref(cfg), byref(pool),
-        None if page_map is None else _int_list(page_map, torch.int32, pool.shape[0], dev, "page_map"),
-        None if n_live is None else _int_list(n_live, torch.int32, 1, dev, "n_live"), ws.data_ptr(),
-        ws.numel() * ws.element_size(), ptr(status), stream_ptr(stream)), "zha_pages_compact")
+        None if page_map is None else _list_ptr(page_map, torch.int32, pool.shape[0], dev, "page_map"),
+        None if n_live is None else _list_ptr(n_live, torch.int32, 1, dev, "n_live"), *_scratch(ws, dev),
+        _status_ptr(status, dev), on), "zha_pages_compact")
