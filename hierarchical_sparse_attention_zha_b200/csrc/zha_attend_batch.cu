@@ -20,16 +20,19 @@
 // A second kernel finds a unit's pieces from the tile counts alone and joins them in a
 // fixed order.
 //
-// Products. A unit has at most 16 query rows, an eighth of a tcgen05 tile, and
-// the call is bound by the cache it reads: the warps' own matrix instructions
-// (16 x 8 x 16 bf16, 16 x 8 x 8 tf32) take their operands from the warp's registers and
-// tile without a hand-over. Their 16 rows hold 8 heads twice, as the first and the
-// following terms of the fp32 operand, or 16 heads.
+// Products. A unit has at most 16 query heads, an eighth of a tcgen05 tile, and the
+// call is bound by the cache it reads and, when it runs for long, by the power that the
+// products take: the warps' own matrix instructions (16 x 8 x 16 bf16, 16 x 8 x 8 tf32)
+// take their operands from the warp's registers and tile without a hand-over. Keys
+// and elements of V are their 16 rows, heads their 8 columns, so that no row is padding:
+// S^T = K Q^T, O^T = V^T P^T. With up to 4 heads the columns hold two terms of the
+// fp32 operand side by side.
 //   bf16 cache: keys and values enter exactly. fp32 queries and weights are three
 //   bf16 terms cut off one after the other (8 + 8 + 8 bits: exact); with bf16
 //   queries, which are exact, weights are two terms (2^-16, below the output's 2^-8).
-//   fp32 cache: every operand is two tf32 terms (2^-23), and the product of the
-//   two second terms (2^-24) is left out where 16 heads fill the rows.
+//   fp32 cache: every operand is two tf32 terms (cut, then rounded: 2^-22), and of
+//   weight times value the product of the two second terms (2^-11 of the weight, 2^-10
+//   of the value) is left out where it would take an instruction of its own.
 #include <cmath>
 
 #include "zha_host.cuh"
@@ -50,7 +53,7 @@ constexpr int kSingleTiles = 32;
 constexpr int kJoinThreads = 256;
 constexpr int kWideUnits = 148;        // up to so many units a CTA joins one head
 
-inline int head_rows(int group) { return group > 8 ? 16 : 8; }
+inline int head_cols(int group) { return group > 8 ? 16 : group > 4 ? 8 : 4; }
 
 struct BatchLayout {
   int64_t units, slots, bytes, slots_off;
@@ -62,7 +65,7 @@ struct BatchLayout {
 // o[d]] for each of the unit's heads.
 inline BatchLayout batch_layout(const Geom& G, int32_t n_seqs) {
   BatchLayout b{};
-  b.hu = head_rows(G.group);
+  b.hu = head_cols(G.group);
   b.hb = (G.group + b.hu - 1) / b.hu;
   b.units = int64_t(n_seqs) * G.hkv * b.hb;
   b.slots = 2 * kMaxWarps;
@@ -124,12 +127,24 @@ __device__ __forceinline__ uint32_t cut_bf16(float& a, float& b) {
   b = b - __uint_as_float(ub & 0xffff0000u);
   return __byte_perm(ua, ub, 0x7632);
 }
-// The next tf32 term of a value, rounded and taken away.
-__device__ __forceinline__ uint32_t cut_tf32(float& a) {
-  uint32_t t;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(t) : "f"(a));
-  a -= __uint_as_float(t);
-  return t;
+// The two tf32 terms of a value: 11 bits cut off, the rest rounded to 11.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& one, uint32_t& two) {
+  one = __float_as_uint(x) & 0xffffe000u;
+  two = (__float_as_uint(x - __uint_as_float(one)) + 0x1000u) & 0xffffe000u;
+}
+
+// Of a weight in [0, 1], which rounding cannot take out of range: both rounded (2^-23).
+__device__ __forceinline__ void split_weight(float x, uint32_t& one, uint32_t& two) {
+  one = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  two = (__float_as_uint(x - __uint_as_float(one)) + 0x1000u) & 0xffffe000u;
+}
+
+// An 8 x 8 matrix of 16-bit values turned over its diagonal: lane (g, t) gives row g,
+// columns 2 t and 2 t + 1, and gets column g, rows 2 t and 2 t + 1.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // ---- tiles ------------------------------------------------------------------
@@ -169,270 +184,261 @@ __device__ __forceinline__ void next_unit(const BatchArgs& A, Place& p) {
   p.end += tiles_of<KEYS>(p.n);
 }
 
-// A warp's query rows as matrix operands. Lane (g, t) = (lane / 4, lane % 4)
-// has rows g and g + 8; the order of the head's elements within a step is that of the K
-// reads: lane t's piece of 16 bytes serves two steps.
+// What a lane (g, t) = (lane / 4, lane % 4) has of the columns: 2 t and 2 t + 1 of a
+// product, g of an operand. Column c of tile q is head c % HU + 8 q, and (HU 4) term
+// c / HU of the pair of terms that an instruction takes.
+template <int HU>
+struct Columns {
+  static constexpr int kTiles = HU == 16 ? 2 : 1;
+  static constexpr int kTerms = HU == 4 ? 2 : 1;             // terms side by side
+  __device__ static int head(int q, int t, int e) { return HU == 4 ? 2 * (t & 1) + e : 8 * q + 2 * t + e; }
+};
+
+// Queries as operands: [step][tile][instruction][2]. The order of a head's elements
+// within a step is that of the K reads: lane t's piece of 16 bytes serves two steps.
 template <typename Kv, typename Qt, int D, int HU>
-struct Queries;
+struct Queries {
+  static constexpr bool kBf = sizeof(Kv) == 2;
+  static constexpr int kSteps = kBf ? D / 16 : D / 8;
+  static constexpr int kTerms = kBf ? (sizeof(Qt) == 2 ? 1 : 3) : 2;
+  static constexpr int kTiles = Columns<HU>::kTiles, kSide = Columns<HU>::kTerms;
+  static constexpr int kOps = (kTerms + kSide - 1) / kSide;
+  uint32_t b[kSteps][kTiles][kOps][2];
 
-template <typename Qt, int D, int HU>
-struct Queries<__nv_bfloat16, Qt, D, HU> {
-  static constexpr bool kExact = sizeof(Qt) == 2;          // one term
-  static constexpr int kSteps = D / 16;
-  static constexpr int kMore = kExact ? 0 : HU == 16 ? 4 : 1;
-  uint32_t a[kSteps][HU == 16 ? 4 : kExact ? 2 : 4];       // first terms of rows g, g + 8 (HU 8: rows g; second terms)
-  uint32_t b[kSteps][kMore == 0 ? 1 : kMore * (HU == 16 ? 1 : 2)];   // HU 16: second, third terms; HU 8: third
+  // Operand register i of step st from the terms of its value (a pair of values).
+  __device__ __forceinline__ void put(int st, int q, int i, const uint32_t (&term)[kTerms], int side) {
+#pragma unroll
+    for (int k = 0; k < kOps; ++k) {
+      if constexpr (kSide == 1) {
+        b[st][q][k][i] = term[k];
+      } else {
+        const uint32_t first = term[2 * k], second = 2 * k + 1 < kTerms ? term[min(2 * k + 1, kTerms - 1)] : 0u;
+        b[st][q][k][i] = side ? second : first;
+      }
+    }
+  }
 
-  __device__ void load(const Qt* q, int heads, int lane) {
-    const int g = lane / 4, t = lane % 4;
+  __device__ void load(const Qt* queries, int heads, int lane) {
+    const int g = lane / 4, t = lane % 4, side = HU == 4 ? g / 4 : 0;
 #pragma unroll
-    for (int r = 0; r < HU / 8; ++r) {
-      const int h = g + 8 * r;
+    for (int q = 0; q < kTiles; ++q) {
+      const int h = HU == 4 ? g % 4 : g + 8 * q;
+      const Qt* row = queries + h * D;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        float v[8] = {};
-        if (h < heads) {
-          if constexpr (kExact) {
-            load_slice<8>(q + h * D, 32 * j + 8 * t, v);
-          } else {
-            float x[4], y[4];
-            load_slice<4>(q + h * D, 32 * j + 8 * t, x);
-            load_slice<4>(q + h * D, 32 * j + 8 * t + 4, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { v[i] = x[i]; v[4 + i] = y[i]; }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {                        // step 2j + i / 2, first or second half of its elements
-          const int st = 2 * j + i / 2, hi = i % 2;
-          const uint32_t one = cut_bf16(v[2 * i], v[2 * i + 1]);
-          if constexpr (kExact) {
-            a[st][HU == 16 ? r + 2 * hi : hi] = one;
-          } else {
-            const uint32_t two = cut_bf16(v[2 * i], v[2 * i + 1]), three = cut_bf16(v[2 * i], v[2 * i + 1]);
-            if constexpr (HU == 16) {
-              a[st][r + 2 * hi] = one;
-              b[st][r + 2 * hi] = two;
-              c[st][r + 2 * hi] = three;
+      for (int j = 0; j < kSteps / 2; ++j) {
+        if constexpr (kBf) {
+          float v[8] = {};
+          if (h < heads) {
+            if constexpr (sizeof(Qt) == 2) {
+              load_slice<8>(row, 32 * j + 8 * t, v);
             } else {
-              a[st][2 * hi] = one;
-              a[st][2 * hi + 1] = two;
-              b[st][hi] = three;
+              float x[4], y[4];
+              load_slice<4>(row, 32 * j + 8 * t, x);
+              load_slice<4>(row, 32 * j + 8 * t + 4, y);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) { v[i] = x[i]; v[4 + i] = y[i]; }
             }
           }
-        }
-      }
-    }
-  }
-  uint32_t c[kSteps][kMore == 4 ? 4 : 1];
-
-  // s[n tile][2 r + e]: row g + 8 r, key 8 * tile + 2 t + e.
-  template <int NT>
-  __device__ void scores(const char* tile, int lane, float (&s)[NT][4]) const {
-    const int g = lane / 4, t = lane % 4;
-    float low[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+          for (int i = 0; i < 4; ++i) {
+            uint32_t term[kTerms];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = low[n][i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 k = *reinterpret_cast<const uint4*>(tile + Tile<__nv_bfloat16, D>::at_k(8 * n + g, 4 * j + t));
-        const uint32_t kb[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int st = 2 * j + u;
-          if constexpr (HU == 16) {
-            mma_bf16(s[n], a[st][0], a[st][1], a[st][2], a[st][3], kb[2 * u], kb[2 * u + 1]);
-            if constexpr (!kExact) {
-              mma_bf16(low[n], b[st][0], b[st][1], b[st][2], b[st][3], kb[2 * u], kb[2 * u + 1]);
-              mma_bf16(low[n], c[st][0], c[st][1], c[st][2], c[st][3], kb[2 * u], kb[2 * u + 1]);
-            }
-          } else if constexpr (kExact) {
-            mma_bf16(s[n], a[st][0], 0u, a[st][1], 0u, kb[2 * u], kb[2 * u + 1]);
-          } else {
-            mma_bf16(s[n], a[st][0], a[st][1], a[st][2], a[st][3], kb[2 * u], kb[2 * u + 1]);
-            mma_bf16(low[n], 0u, b[st][0], 0u, b[st][1], kb[2 * u], kb[2 * u + 1]);
+            for (int k = 0; k < kTerms; ++k) term[k] = cut_bf16(v[2 * i], v[2 * i + 1]);
+            put(2 * j + i / 2, q, i % 2, term, side);
           }
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (HU == 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
-      } else {
-        s[n][0] += s[n][2] + low[n][2];
-        s[n][1] += s[n][3] + low[n][3];
-      }
-    }
-  }
-};
-
-template <typename Qt, int D, int HU>
-struct Queries<float, Qt, D, HU> {
-  static constexpr int kSteps = D / 8;
-  uint32_t a[kSteps][4];                                     // HU 8: rows g first terms, rows g + 8 second terms
-  uint32_t b[HU == 16 ? kSteps : 1][4];                      // HU 16: second terms
-
-  __device__ void load(const Qt* q, int heads, int lane) {
-    const int g = lane / 4, t = lane % 4;
-#pragma unroll
-    for (int r = 0; r < HU / 8; ++r) {
-      const int h = g + 8 * r;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        float v[4] = {};
-        if (h < heads) load_slice<4>(q + h * D, 16 * j + 4 * t, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int st = 2 * j + i / 2, hi = i % 2;
-          const uint32_t one = cut_tf32(v[i]), two = cut_tf32(v[i]);
-          a[st][2 * hi + r] = one;
-          if constexpr (HU == 16) b[st][2 * hi + r] = two;
-          else a[st][2 * hi + 1] = two;
-        }
-      }
-    }
-  }
-
-  template <int NT>
-  __device__ void scores(const char* tile, int lane, float (&s)[NT][4]) const {
-    const int g = lane / 4, t = lane % 4;
-    float low[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = low[n][i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float4 k = *reinterpret_cast<const float4*>(tile + Tile<float, D>::at_k(8 * n + g, 4 * j + t));
-        float kr[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int st = 2 * j + u;
-          const uint32_t h0 = cut_tf32(kr[2 * u]), h1 = cut_tf32(kr[2 * u + 1]);
-          const uint32_t l0 = cut_tf32(kr[2 * u]), l1 = cut_tf32(kr[2 * u + 1]);
-          mma_tf32(s[n], a[st][0], a[st][1], a[st][2], a[st][3], h0, h1);
-          mma_tf32(low[n], a[st][0], a[st][1], a[st][2], a[st][3], l0, l1);
-          if constexpr (HU == 16) mma_tf32(low[n], b[st][0], b[st][1], b[st][2], b[st][3], h0, h1);
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
-      if constexpr (HU == 8) {
-        s[n][0] += s[n][2];
-        s[n][1] += s[n][3];
-      }
-    }
-  }
-};
-
-// o[n tile] += weights * V. p[n tile][2 r + e] as the scores.
-template <int D, int HU, int TERMS, int NT>
-__device__ __forceinline__ void add_values(const __nv_bfloat16*, uint32_t tile, const char*, int lane, float (&p)[NT][4],
-                                           float (&o)[D / 8][4]) {
-#pragma unroll
-  for (int kb = 0; kb < NT / 2; ++kb) {
-    uint32_t w[TERMS][4];                                    // [term][element half * 2 + row]: a0..a3 of 16 rows
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int r = 0; r < HU / 8; ++r)
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) w[k][2 * half + r] = cut_bf16(p[2 * kb + half][2 * r], p[2 * kb + half][2 * r + 1]);
-    const int row = kb * 16 + (lane & 15);
-#pragma unroll
-    for (int n0 = 0; n0 < D / 16; n0 += 4) {                 // 64 elements: every term in turn on 8 tiles of o
-      uint32_t v[8][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v[2 * i][0]), "=r"(v[2 * i][1]), "=r"(v[2 * i + 1][0]), "=r"(v[2 * i + 1][1])
-                     : "r"(tile + Tile<__nv_bfloat16, D>::at_v(row, 2 * (n0 + i) + (lane >> 4)))
-                     : "memory");
-      if constexpr (HU == 16) {
-#pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mma_bf16(o[2 * n0 + i], w[k][0], w[k][1], w[k][2], w[k][3], v[i][0], v[i][1]);
-      } else {
-        if constexpr (TERMS == 3) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mma_bf16(o[2 * n0 + i], 0u, w[2][0], 0u, w[2][2], v[i][0], v[i][1]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16(o[2 * n0 + i], w[0][0], w[1][0], w[0][2], w[1][2], v[i][0], v[i][1]);
-      }
-    }
-  }
-}
-
-// fp32: within a tile of 8 keys, the step's elements t and t + 4 are the keys 2 t and
-// 2 t + 1, which is how the scores lie.
-template <int D, int HU, int TERMS, int NT>
-__device__ __forceinline__ void add_values(const float*, uint32_t, const char* tile, int lane, float (&p)[NT][4],
-                                           float (&o)[D / 8][4]) {
-  const int g = lane / 4, t = lane % 4;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    uint32_t w[2][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int r = 0; r < HU / 8; ++r) {
-        w[0][2 * e + r] = cut_tf32(p[n][2 * r + e]);
-        w[1][2 * e + r] = cut_tf32(p[n][2 * r + e]);
-      }
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const float4 x = *reinterpret_cast<const float4*>(tile + Tile<float, D>::at_v(8 * n + 2 * t, 8 * j + g));
-      const float4 y = *reinterpret_cast<const float4*>(tile + Tile<float, D>::at_v(8 * n + 2 * t + 1, 8 * j + g));
-      float vx[4] = {x.x, x.y, x.z, x.w}, vy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t h0 = cut_tf32(vx[i]), h1 = cut_tf32(vy[i]), l0 = cut_tf32(vx[i]), l1 = cut_tf32(vy[i]);
-        float(&c)[4] = o[4 * j + i];
-        if constexpr (HU == 16) {
-          mma_tf32(c, w[0][0], w[0][1], w[0][2], w[0][3], l0, l1);
-          mma_tf32(c, w[1][0], w[1][1], w[1][2], w[1][3], h0, h1);
-          mma_tf32(c, w[0][0], w[0][1], w[0][2], w[0][3], h0, h1);
         } else {
-          mma_tf32(c, w[0][0], w[1][0], w[0][2], w[1][2], l0, l1);
-          mma_tf32(c, w[0][0], w[1][0], w[0][2], w[1][2], h0, h1);
+          float v[4] = {};
+          if (h < heads) load_slice<4>(row, 16 * j + 4 * t, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t term[kTerms];
+            split_tf32(v[i], term[0], term[1]);
+            put(2 * j + i / 2, q, i % 2, term, side);
+          }
         }
       }
     }
   }
-}
 
-__device__ __forceinline__ void put2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
-__device__ __forceinline__ void put2(__nv_bfloat16* p, float a, float b) {
-  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
-}
-
-// Row r of o times f, lane t4's part of it. Column 2 t4 + e of o's tile i is the head's
-// element 8 i + 2 t4 + e (bf16 V) or 32 (i / 4) + 4 (2 t4 + e) + i % 4 (fp32 V).
-template <typename Kv, int D, typename Dst>
-__device__ __forceinline__ void put_row(Dst* row, int t4, int r, float f, const float (&o)[D / 8][4]) {
+  // s[q][block][e]: key 8 * block + g, column 2 t + e.
+  template <int NB>
+  __device__ void scores(const char* tile, int lane, float (&s)[kTiles][NB][2]) const {
+    const int g = lane / 4, t = lane % 4;
+    if constexpr (kBf) {
 #pragma unroll
-  for (int i = 0; i < D / 8; i += sizeof(Kv) == 2 ? 1 : 2) {
-    if constexpr (sizeof(Kv) == 2) {
-      put2(row + 8 * i + 2 * t4, o[i][2 * r] * f, o[i][2 * r + 1] * f);
+      for (int mb = 0; mb < NB / 2; ++mb) {                  // 16 keys
+        float c[kTiles][kOps][4] = {};
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + Tile<Kv, D>::at_k(16 * mb + g, 4 * j + t));
+          const uint4 y = *reinterpret_cast<const uint4*>(tile + Tile<Kv, D>::at_k(16 * mb + 8 + g, 4 * j + t));
+#pragma unroll
+          for (int q = 0; q < kTiles; ++q)
+#pragma unroll
+            for (int k = 0; k < kOps; ++k) {
+              mma_bf16(c[q][k], x.x, y.x, x.y, y.y, b[2 * j][q][k][0], b[2 * j][q][k][1]);
+              mma_bf16(c[q][k], x.z, y.z, x.w, y.w, b[2 * j + 1][q][k][0], b[2 * j + 1][q][k][1]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kTiles; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = c[q][kOps - 1][i];
+#pragma unroll
+            for (int k = kOps - 2; k >= 0; --k) v += c[q][k][i];
+            s[q][2 * mb + i / 2][i % 2] = v;
+          }
+      }
     } else {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        put2(row + 32 * (i / 4) + 4 * (2 * t4 + e) + i % 4, o[i][2 * r + e] * f, o[i + 1][2 * r + e] * f);
+      for (int n = 0; n < NB; ++n) {                         // 8 keys: rows g first terms, rows g + 8 second terms
+        float c[kTiles][kOps][4] = {};
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const float4 x = *reinterpret_cast<const float4*>(tile + Tile<Kv, D>::at_k(8 * n + g, 4 * j + t));
+          uint32_t one[4], two[4];
+          split_tf32(x.x, one[0], two[0]);
+          split_tf32(x.y, one[1], two[1]);
+          split_tf32(x.z, one[2], two[2]);
+          split_tf32(x.w, one[3], two[3]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int q = 0; q < kTiles; ++q)
+#pragma unroll
+              for (int k = 0; k < kOps; ++k)
+                mma_tf32(c[q][k], one[2 * u], two[2 * u], one[2 * u + 1], two[2 * u + 1], b[2 * j + u][q][k][0],
+                         b[2 * j + u][q][k][1]);
+        }
+#pragma unroll
+        for (int q = 0; q < kTiles; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float low = c[q][0][2 + e];
+#pragma unroll
+            for (int k = 1; k < kOps; ++k) low += c[q][k][e] + c[q][k][2 + e];
+            s[q][n][e] = c[q][0][e] + low;
+          }
+      }
+    }
+    if constexpr (kSide == 2) {                              // the two terms' parts
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) s[0][n][e] += __shfl_xor_sync(0xffffffffu, s[0][n][e], 2);
     }
   }
+};
+
+// o[q][tile of 16 elements] += V^T * weights; p as the scores.
+template <typename Kv, int D, int HU, int TERMS, int NB>
+__device__ __forceinline__ void add_values(uint32_t tile_at, const char* tile, int lane,
+                                           float (&p)[Columns<HU>::kTiles][NB][2],
+                                           float (&o)[Columns<HU>::kTiles][D / 16][4]) {
+  constexpr int kTiles = Columns<HU>::kTiles, kSide = Columns<HU>::kTerms, kOps = (TERMS + kSide - 1) / kSide;
+  const int g = lane / 4, t = lane % 4;
+  const bool second = kSide == 2 && t >= 2;
+  if constexpr (sizeof(Kv) == 2) {
+#pragma unroll
+    for (int mb = 0; mb < NB / 2; ++mb) {
+      uint32_t w[kTiles][kOps][2];
+#pragma unroll
+      for (int q = 0; q < kTiles; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* v = p[q][2 * mb + i];
+          uint32_t term[TERMS];
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) term[k] = cut_bf16(v[0], v[1]);
+#pragma unroll
+          for (int k = 0; k < kOps; ++k) {
+            uint32_t x = term[kSide * k];
+            if constexpr (kSide == 2)
+              if (second) x = 2 * k + 1 < TERMS ? term[min(2 * k + 1, TERMS - 1)] : 0u;
+            w[q][k][i] = transposed(x);
+          }
+        }
+      const int row = 16 * mb + (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+      for (int d0 = 0; d0 < D / 16; d0 += 4) {               // 64 elements: every term in turn on 4 tiles of o
+        uint32_t v[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
+                       : "r"(tile_at + Tile<Kv, D>::at_v(row, 2 * (d0 + i) + ((lane >> 3) & 1)))
+                       : "memory");
+#pragma unroll
+        for (int k = kOps - 1; k >= 0; --k)
+#pragma unroll
+          for (int q = 0; q < kTiles; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_bf16(o[q][d0 + i], v[i][0], v[i][1], v[i][2], v[i][3], w[q][k][0], w[q][k][1]);
+      }
+    }
+  } else {
+    // Within 8 keys, the step's elements t and t + 4 are the keys 2 t and 2 t + 1.
+    // Rows g and g + 8 of tile 4 j + i are the elements 64 j + 4 g + i and 32 more.
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      uint32_t w[kTiles][kOps][2];
+#pragma unroll
+      for (int q = 0; q < kTiles; ++q) {
+        uint32_t one[2], two[2];
+        split_weight(p[q][n][0], one[0], two[0]);
+        split_weight(p[q][n][1], one[1], two[1]);
+#pragma unroll
+        for (int k = 0; k < kOps; ++k) {
+          const uint32_t x = (kSide == 2 ? second : k == 1) ? two[0] : one[0];
+          const uint32_t y = (kSide == 2 ? second : k == 1) ? two[1] : one[1];
+          const uint32_t lo = transposed(__byte_perm(x, y, 0x5410)), hi = transposed(__byte_perm(x, y, 0x7632));
+          w[q][k][0] = __byte_perm(lo, hi, 0x5410);
+          w[q][k][1] = __byte_perm(lo, hi, 0x7632);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const float4 a = *reinterpret_cast<const float4*>(tile + Tile<Kv, D>::at_v(8 * n + 2 * t, 16 * j + g));
+        const float4 b = *reinterpret_cast<const float4*>(tile + Tile<Kv, D>::at_v(8 * n + 2 * t, 16 * j + 8 + g));
+        const float4 c = *reinterpret_cast<const float4*>(tile + Tile<Kv, D>::at_v(8 * n + 2 * t + 1, 16 * j + g));
+        const float4 d = *reinterpret_cast<const float4*>(tile + Tile<Kv, D>::at_v(8 * n + 2 * t + 1, 16 * j + 8 + g));
+        const float v[4][4] = {{a.x, b.x, c.x, d.x}, {a.y, b.y, c.y, d.y}, {a.z, b.z, c.z, d.z}, {a.w, b.w, c.w, d.w}};
+        uint32_t one[4][4], two[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) split_tf32(v[i][r], one[i][r], two[i][r]);
+#pragma unroll
+        for (int q = 0; q < kTiles; ++q) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_tf32(o[q][4 * j + i], two[i][0], two[i][1], two[i][2], two[i][3], w[q][0][0], w[q][0][1]);
+#pragma unroll
+          for (int k = kOps - 1; k >= 0; --k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_tf32(o[q][4 * j + i], one[i][0], one[i][1], one[i][2], one[i][3], w[q][k][0], w[q][k][1]);
+        }
+      }
+    }
+  }
+}
+
+// The element of the head in row g + 8 r of o's tile.
+template <typename Kv>
+__device__ __forceinline__ int element_of(int tile, int r, int g) {
+  return sizeof(Kv) == 2 ? 16 * tile + 8 * r + g : 64 * (tile / 4) + 32 * r + 4 * g + tile % 4;
+}
+
+// Column e of o's tiles times f, lane g's elements of a head's row.
+template <typename Kv, int D, typename Dst>
+__device__ __forceinline__ void put_row(Dst* row, int g, int e, float f, const float (&o)[D / 16][4]) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) store_o(row + element_of<Kv>(i, r, g), o[i][2 * r + e] * f);
 }
 
 struct BatchSmem {
@@ -448,7 +454,7 @@ constexpr size_t kBatchSmem = kRingBytes + sizeof(BatchSmem);
 template <typename Kv, typename Qt, int D, int HU>
 __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchArgs A) {
   using T = Tile<Kv, D>;
-  constexpr int KEYS = T::kKeys, NT = KEYS / 8, NH = HU / 8;
+  constexpr int KEYS = T::kKeys, NB = KEYS / 8, NQ = Columns<HU>::kTiles;
   constexpr int TERMS = sizeof(Kv) == 4 || sizeof(Qt) == 2 ? 2 : 3;
   extern __shared__ __align__(128) char smem[];
   BatchSmem& J = *reinterpret_cast<BatchSmem*>(smem + kRingBytes);
@@ -572,7 +578,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
 
   int64_t at = t0;
   int stage = 0;
-  float m[NH], l[NH], o[D / 8][4];
+  float m[NQ][2], l[NQ][2], o[NQ][D / 16][4];
+  const bool mine = HU != 4 || t4 < 2;                       // of two lanes with the same heads
   if (lane == 0) J.unit[warp] = -1;
   while (at < t1) {
     const int h0 = (cur.ub % A.hb) * HU, heads = min(HU, A.group - h0);
@@ -580,9 +587,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
     Queries<Kv, Qt, D, HU> q;
     q.load(static_cast<const Qt*>(A.Q) + qrow * D, heads, lane);
 #pragma unroll
-    for (int r = 0; r < NH; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+    for (int c = 0; c < NQ; ++c) {
+      m[c][0] = m[c][1] = -INFINITY;
+      l[c][0] = l[c][1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int i = 0; i < D / 16; ++i) o[c][i][0] = o[c][i][1] = o[c][i][2] = o[c][i][3] = 0.f;
+    }
 
     const int64_t stop = min64(t1, cur.end);
     for (; at < stop; ++at) {
@@ -592,84 +602,91 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       __syncwarp();
       const char* tile = ring + stage * 2 * kTileBytes;
       const uint32_t mask = J.mask[warp][stage];
-      float p[NT][4];
+      float p[NQ][NB][2];
       q.scores(tile, lane, p);
-      float top[NH];
-#pragma unroll
-      for (int r = 0; r < NH; ++r) {
-        top[r] = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = p[n][2 * r + e];
-            x = (mask >> (8 * n + 2 * t4 + e)) & 1u ? x * A.scale_log2 : -INFINITY;
-            top[r] = fmaxf(top[r], x);
-          }
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      }
+      float top[NQ][2];
       bool higher = false;
 #pragma unroll
-      for (int r = 0; r < NH; ++r) higher |= top[r] > m[r];
+      for (int c = 0; c < NQ; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            p[c][n][e] = (mask >> (8 * n + g)) & 1u ? p[c][n][e] * A.scale_log2 : -INFINITY;
+            x = fmaxf(x, p[c][n][e]);
+          }
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+          top[c][e] = x;
+          higher |= x > m[c][e];
+        }
       if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
-        for (int r = 0; r < NH; ++r) {
-          const float mn = fmaxf(m[r], top[r]), a = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-          m[r] = mn;
-          l[r] *= a;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][2 * r] *= a;
-            o[i][2 * r + 1] *= a;
-            if constexpr (HU == 8) { o[i][2] *= a; o[i][3] *= a; }
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < NH; ++r) {
-        const float base = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int c = 0; c < NQ; ++c)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float& x = p[n][2 * r + e];
-            x = ex2(x - base);
-            l[r] += x;
+            const float mn = fmaxf(m[c][e], top[c][e]), a = mn == -INFINITY ? 1.f : ex2(m[c][e] - mn);
+            m[c][e] = mn;
+            l[c][e] *= a;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) { o[c][i][e] *= a; o[c][i][2 + e] *= a; }
           }
       }
-      add_values<D, HU, TERMS, NT>(static_cast<const Kv*>(nullptr), ring_at + stage * 2 * kTileBytes + kTileBytes,
-                                   tile + kTileBytes, lane, p, o);
+#pragma unroll
+      for (int c = 0; c < NQ; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = m[c][e] == -INFINITY ? 0.f : m[c][e];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            p[c][n][e] = ex2(p[c][n][e] - base);
+            l[c][e] += p[c][n][e];
+          }
+        }
+      add_values<Kv, D, HU, TERMS, NB>(ring_at + stage * 2 * kTileBytes + kTileBytes, tile + kTileBytes, lane, p, o);
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 
 #pragma unroll
-    for (int r = 0; r < NH; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-    if constexpr (HU == 8) {
+    for (int c = 0; c < NQ; ++c)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) { o[i][0] += o[i][2]; o[i][1] += o[i][3]; }
-    }
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[c][e] += __shfl_xor_sync(0xffffffffu, l[c][e], w);
+        if constexpr (HU == 4) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[c][i][e] += __shfl_xor_sync(0xffffffffu, o[c][i][e], 2);
+            o[c][i][2 + e] += __shfl_xor_sync(0xffffffffu, o[c][i][2 + e], 2);
+          }
+        }
+      }
     const bool starts = cur.first >= t0, ends = cur.end <= t1;
     if (starts && ends) {
 #pragma unroll
-      for (int r = 0; r < NH; ++r)
-        if (g + 8 * r < heads) {
-          const int64_t out = qrow + g + 8 * r;
-          const float f = l[r] == 0.f ? 0.f : 1.f / l[r];
-          put_row<Kv, D>(static_cast<Qt*>(A.O) + out * D, t4, r, f, o);
-          if (t4 == 0 && A.lse != nullptr) A.lse[out] = l[r] == 0.f ? -INFINITY : 0.69314718056f * (m[r] + log2f(l[r]));
+      for (int c = 0; c < NQ; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = Columns<HU>::head(c, t4, e);
+          if (h < heads && mine) {
+            const int64_t out = qrow + h;
+            const float L = l[c][e];
+            put_row<Kv, D>(static_cast<Qt*>(A.O) + out * D, g, e, L == 0.f ? 0.f : 1.f / L, o[c]);
+            if (g == 0 && A.lse != nullptr) A.lse[out] = L == 0.f ? -INFINITY : 0.69314718056f * (m[c][e] + log2f(L));
+          }
         }
     } else if (cur.end < t1) {
       float* piece = A.slots + (kMaxWarps + int64_t(blockIdx.x) * kWarps + warp) * HU * (D + 4);
 #pragma unroll
-      for (int r = 0; r < NH; ++r) {
-        float* slot = piece + (g + 8 * r) * (D + 4);
-        put_row<Kv, D>(slot + 4, t4, r, 1.f, o);
-        if (t4 == 0) { slot[0] = m[r]; slot[1] = l[r]; }
-      }
+      for (int c = 0; c < NQ; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (mine) {
+            float* slot = piece + Columns<HU>::head(c, t4, e) * (D + 4);
+            put_row<Kv, D>(slot + 4, g, e, 1.f, o[c]);
+            if (g == 0) { slot[0] = m[c][e]; slot[1] = l[c][e]; }
+          }
     } else if (lane == 0) {
       J.unit[warp] = int64_t(cur.s) * per + cur.ub;
       J.starts[warp] = starts;
@@ -685,10 +702,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
   float* states = reinterpret_cast<float*>(smem);            // [warp][HU][D]
   if (J.unit[warp] >= 0) {
 #pragma unroll
-    for (int r = 0; r < NH; ++r) {
-      put_row<Kv, D>(states + (warp * HU + g + 8 * r) * D, t4, r, 1.f, o);
-      if (t4 == 0) { J.m[warp][g + 8 * r] = m[r]; J.l[warp][g + 8 * r] = l[r]; }
-    }
+    for (int c = 0; c < NQ; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (mine) {
+          const int h = Columns<HU>::head(c, t4, e);
+          put_row<Kv, D>(states + (warp * HU + h) * D, g, e, 1.f, o[c]);
+          if (g == 0) { J.m[warp][h] = m[c][e]; J.l[warp][h] = l[c][e]; }
+        }
   }
   __syncthreads();
   for (int a = 0, b; a < kWarps; a = b) {
@@ -832,15 +853,18 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
 
 template <typename Kv, typename Qt>
 cudaError_t launch_batch_d(const BatchArgs& A, int d, cudaStream_t s) {
-  if (head_rows(A.group) == 16) return d == 128 ? launch_batch<Kv, Qt, 128, 16>(A, s) : launch_batch<Kv, Qt, 64, 16>(A, s);
-  return d == 128 ? launch_batch<Kv, Qt, 128, 8>(A, s) : launch_batch<Kv, Qt, 64, 8>(A, s);
+  switch (head_cols(A.group)) {
+    case 4: return d == 128 ? launch_batch<Kv, Qt, 128, 4>(A, s) : launch_batch<Kv, Qt, 64, 4>(A, s);
+    case 8: return d == 128 ? launch_batch<Kv, Qt, 128, 8>(A, s) : launch_batch<Kv, Qt, 64, 8>(A, s);
+    default: return d == 128 ? launch_batch<Kv, Qt, 128, 16>(A, s) : launch_batch<Kv, Qt, 64, 16>(A, s);
+  }
 }
 
 // Units beyond this are refused: slots and grids stay far below 2^31.
 constexpr int64_t kMaxUnits = int64_t(1) << 22;
 
 bool units_ok(const Geom& G, int32_t n_seqs) {
-  const int64_t hb = (G.group + head_rows(G.group) - 1) / head_rows(G.group);
+  const int64_t hb = (G.group + head_cols(G.group) - 1) / head_cols(G.group);
   return int64_t(G.hkv) * hb <= kMaxUnits / n_seqs;
 }
 
