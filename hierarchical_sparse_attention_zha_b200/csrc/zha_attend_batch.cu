@@ -85,6 +85,7 @@ struct BatchArgs {
   float* slots;
   int32_t* status;
   int32_t n_seqs, hkv, hq, group, hb, chunk, single;
+  uint32_t div_mul, div_shift;          // t / chunk = t * div_mul >> div_shift for t < 2^31
   float scale_log2;                     // log2(e) / sqrt(d)
 };
 
@@ -99,6 +100,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // 16 bytes into shared memory, or 16 zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(take ? 16 : 0) : "memory");
 }
@@ -544,14 +548,25 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
   Place ahead = cur;
   int64_t next = t0;
   int32_t row = -1;
+  int64_t head = t0 < t1 ? int64_t(cur.s) * A.hkv + cur.ub / A.hb : 0;
   auto look_up = [&] {
     row = -1;
     if (next >= t1) return;
-    while (next >= ahead.end) next_unit<KEYS>(A, ahead);
+    while (next >= ahead.end) {
+      next_unit<KEYS>(A, ahead);
+      head = int64_t(ahead.s) * A.hkv + ahead.ub / A.hb;
+    }
     const int64_t tok = (next - ahead.first) * KEYS + lane;
     if (lane < KEYS && tok < ahead.n) {
-      row = kv_batch_row(A.kv, A.hkv, ahead.s, ahead.ub / A.hb, tok, A.chunk);
-      if (row < 0 && A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_PAGE);
+      const uint32_t t = uint32_t(tok);
+      if (A.kv.table == nullptr) {
+        row = int32_t(head) * int32_t(A.kv.ld) + int32_t(t);
+      } else {
+        const uint32_t block = uint32_t(uint64_t(t) * A.div_mul >> A.div_shift);
+        const int32_t page = A.kv.table[head * A.kv.max_blocks + block];
+        if (page >= 0 && page < A.kv.ld) row = page * A.chunk + int32_t(t - block * A.chunk);
+        else if (A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_PAGE);
+      }
     }
   };
   auto issue = [&](int stage) {
@@ -559,13 +574,28 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
       if (lane == 0) J.mask[warp][stage] = mask;
       const uint32_t to = ring_at + stage * 2 * kTileBytes;
+      const int piece = lane % T::kPieces, key0 = lane / T::kPieces;
+      constexpr int kStep = 32 / T::kPieces;                 // keys of a round of 32 pieces
+      const int32_t first = __shfl_sync(0xffffffffu, row, 0);
+      if (__all_sync(0xffffffffu, lane >= KEYS || (row == first + lane && first >= 0))) {
+        // rows one behind the other: one address
+        const int64_t off = int64_t(first) * T::kRow + lane * 16;
+        const char* k = static_cast<const char*>(A.kv.k) + off;
+        const char* v = static_cast<const char*>(A.kv.v) + off;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = (i * 32 + lane) / T::kPieces, piece = lane % T::kPieces;
-        const int32_t r = __shfl_sync(0xffffffffu, row, key);
-        const int64_t off = int64_t(max(r, 0)) * T::kRow + piece * 16;
-        copy16(to + T::at_k(key, piece), static_cast<const char*>(A.kv.k) + off, r >= 0);
-        copy16(to + kTileBytes + T::at_v(key, piece), static_cast<const char*>(A.kv.v) + off, r >= 0);
+        for (int i = 0; i < 8; ++i) {
+          copy16(to + T::at_k(i * kStep + key0, piece), k + i * 512);
+          copy16(to + kTileBytes + T::at_v(i * kStep + key0, piece), v + i * 512);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = i * kStep + key0;
+          const int32_t r = __shfl_sync(0xffffffffu, row, key);
+          const int64_t off = int64_t(max(r, 0)) * T::kRow + piece * 16;
+          copy16(to + T::at_k(key, piece), static_cast<const char*>(A.kv.k) + off, r >= 0);
+          copy16(to + kTileBytes + T::at_v(key, piece), static_cast<const char*>(A.kv.v) + off, r >= 0);
+        }
       }
       ++next;
       look_up();
@@ -604,6 +634,13 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       const uint32_t mask = J.mask[warp][stage];
       float p[NQ][NB][2];
       q.scores(tile, lane, p);
+      if (mask != (KEYS == 32 ? ~0u : (1u << (KEYS % 32)) - 1)) {
+#pragma unroll
+        for (int c = 0; c < NQ; ++c)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+            if (!((mask >> (8 * n + g)) & 1u)) p[c][n][0] = p[c][n][1] = -INFINITY;
+      }
       float top[NQ][2];
       bool higher = false;
 #pragma unroll
@@ -613,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
           float x = -INFINITY;
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
-            p[c][n][e] = (mask >> (8 * n + g)) & 1u ? p[c][n][e] * A.scale_log2 : -INFINITY;
+            p[c][n][e] *= A.scale_log2;
             x = fmaxf(x, p[c][n][e]);
           }
 #pragma unroll
@@ -916,6 +953,9 @@ zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q
   A.group = G.group;
   A.hb = lay.hb;
   A.chunk = G.chunk;
+  A.div_shift = 31;
+  while ((1 << (A.div_shift - 31)) < G.chunk) ++A.div_shift;
+  A.div_mul = uint32_t(((uint64_t(1) << A.div_shift) + G.chunk - 1) / G.chunk);
   A.scale_log2 = float(1.4426950408889634 / std::sqrt(double(G.d)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using bf = __nv_bfloat16;
