@@ -7,8 +7,10 @@
 //
 // Split. A unit is (sequence, KV head, block of its query heads); its keys are cut
 // into tiles of 4 KB of K and 4 KB of V. All units' tiles, one behind the other, are
-// dealt out evenly to the warps (warp w has tiles [w T / n, (w + 1) T / n)), from the
-// counts in device memory, so that ragged lengths cost nothing. A warp keeps its own
+// dealt out evenly to the warps from the counts in device memory, so that ragged
+// lengths cost nothing. SMs do not read equally fast (240K tokens: their shares took 58
+// to 78 us), so a long call deals 7/8 of the tiles to the CTAs that the GPU holds at
+// a time, and the rest to as many more, which the SMs that are done first take. A warp keeps its own
 // ring of tiles in flight (cp.async), across the borders of units, and waits for no
 // other until its tiles are done. What then becomes of a unit's state:
 //   - all of its tiles in one warp: the warp writes the result;
@@ -46,8 +48,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;              // tiles in a warp's ring
 constexpr int kTileBytes = 4096;        // of K, and of V
-constexpr int kMaxCtas = 148 * 2;
+constexpr int kMaxSms = 148;
+constexpr int kMaxCtas = kMaxSms * 4;   // two a SM at a time, twice
 constexpr int kMaxWarps = kMaxCtas * kWarps;
+constexpr int kTwoTiers = 24;           // tiles a warp from which the second deal pays
 constexpr int kMinTiles = 2;            // no warp takes less, unless there is less
 constexpr int kSingleTiles = 32;
 constexpr int kJoinThreads = 256;
@@ -61,7 +65,7 @@ struct BatchLayout {
 };
 
 // Workspace: int64 prefix[n_seqs + 1] (tiles of one unit of the sequences
-// before s), int64 warp count; then the group pieces and the end pieces, [m, l, 0, 0,
+// before s); then the group pieces and the end pieces, [m, l, 0, 0,
 // o[d]] for each of the unit's heads.
 inline BatchLayout batch_layout(const Geom& G, int32_t n_seqs) {
   BatchLayout b{};
@@ -69,7 +73,7 @@ inline BatchLayout batch_layout(const Geom& G, int32_t n_seqs) {
   b.hb = (G.group + b.hu - 1) / b.hu;
   b.units = int64_t(n_seqs) * G.hkv * b.hb;
   b.slots = 2 * kMaxWarps;
-  b.slots_off = round_up((int64_t(n_seqs) + 2) * 8, 256);
+  b.slots_off = round_up((int64_t(n_seqs) + 1) * 8, 256);
   b.bytes = b.slots_off + round_up(b.slots * b.hu * (G.d + 4) * 4, 256);
   return b;
 }
@@ -85,6 +89,7 @@ struct BatchArgs {
   float* slots;
   int32_t* status;
   int32_t n_seqs, hkv, hq, group, hb, chunk, single;
+  int32_t first_ctas, ctas;             // of the first deal, of both
   uint32_t div_mul, div_shift;          // t / chunk = t * div_mul >> div_shift for t < 2^31
   float scale_log2;                     // log2(e) / sqrt(d)
 };
@@ -92,6 +97,17 @@ struct BatchArgs {
 // ---- small pieces -----------------------------------------------------------
 __device__ __forceinline__ void store_o(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_o(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  uint2 x;
+  __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+  x.x = *reinterpret_cast<uint32_t*>(&lo);
+  x.y = *reinterpret_cast<uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p) = x;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -176,6 +192,41 @@ __device__ __forceinline__ int64_t clamped(const BatchArgs& A, int s) {
 }
 template <int KEYS>
 __device__ __forceinline__ int64_t tiles_of(int64_t n) { return (n + KEYS - 1) / KEYS; }
+
+// (The hardware has no integer division: 32-bit ones take a fifth of the 64-bit ones.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
+// n tiles dealt to w warps: the first r get q + 1.
+struct Even {
+  int64_t q, r;
+  __device__ Even(int64_t n, int64_t w) : q(quotient(n, w)), r(n - q * w) {}
+  __device__ int64_t start(int64_t w) const { return w * q + min64(w, r); }
+  __device__ int64_t owner(int64_t t) const {
+    const int64_t more = r * (q + 1);
+    return t < more ? quotient(t, q + 1) : r + quotient(t - more, q);
+  }
+};
+
+// All tiles dealt to the warps of both tiers.
+struct Deal {
+  int64_t total, n1, w1, w2;
+  Even one, two;
+  __device__ static int64_t first_tiles(const BatchArgs& A, int64_t n) {
+    return A.ctas > A.first_ctas && n >= int64_t(kTwoTiers) * kWarps * A.first_ctas ? n - n / 8 : n;
+  }
+  __device__ static int64_t first_warps(const BatchArgs& A, int64_t n) {
+    return max64(1, min64(int64_t(A.first_ctas) * kWarps, (n + kMinTiles - 1) / kMinTiles));
+  }
+  __device__ Deal(const BatchArgs& A, int64_t n)
+      : total(n), n1(first_tiles(A, n)), w1(first_warps(A, n)), w2(max64(1, int64_t(A.ctas - A.first_ctas) * kWarps)),
+        one(n1, w1), two(n - n1, w2) {}
+  __device__ int64_t start(int64_t w) const {
+    return w <= w1 ? one.start(w) : n1 == total ? total : n1 + two.start(min64(w - w1, w2));
+  }
+  __device__ int64_t owner(int64_t t) const { return t < n1 ? one.owner(t) : w1 + two.owner(t - n1); }
+};
 
 // To the next unit that has tiles; the caller knows that there is one.
 template <int KEYS>
@@ -488,8 +539,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       return;
     }
     const int n_w = int(min64(kWarps, cur.end));
-    t0 = warp < n_w ? warp * cur.end / n_w : cur.end;
-    t1 = warp < n_w ? (warp + 1) * cur.end / n_w : cur.end;
+    const int tiles = int(cur.end), each = tiles / n_w, more = tiles - each * n_w;     // at most kSingleTiles
+    t0 = min(tiles, warp * each + min(warp, more));
+    t1 = min(tiles, (warp + 1) * each + min(warp + 1, more));
   } else {
     // Tiles of all sequences and where this CTA's warps begin. Thread i scans a run of
     // ceil(S / threads) sequences.
@@ -512,32 +564,32 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       all += J.scan[w];
     }
     const int64_t total = all * per;
-    const int64_t n_w = max64(1, min64(int64_t(gridDim.x) * kWarps, (total + kMinTiles - 1) / kMinTiles));
+    const Deal deal(A, total);
     const int64_t w0 = int64_t(blockIdx.x) * kWarps;
+    int64_t starts[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) starts[w] = deal.start(w0 + w);
     for (int s = s0; s < s1; ++s) {
       const int64_t n = A.n_tokens[s], tl = tiles_of<KEYS>(clamped(A, s));
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const int64_t t = w0 + w < n_w ? (w0 + w) * total / n_w : total;
-        if (t >= at * per && t < (at + tl) * per) { J.at[w][0] = s; J.at[w][1] = at; }
-      }
+      for (int w = 0; w < kWarps; ++w)
+        if (starts[w] >= at * per && starts[w] < (at + tl) * per) { J.at[w][0] = s; J.at[w][1] = at; }
       if (blockIdx.x == 0) {
         A.prefix[s] = at;
         if ((n < 0 || n > A.max_tokens) && A.status != nullptr) atomicOr(A.status, ZHA_DEV_BAD_LENGTH);
       }
       at += tl;
     }
-    if (blockIdx.x == 0 && tid == 0) { A.prefix[A.n_seqs] = all; A.prefix[A.n_seqs + 1] = n_w; }
+    if (blockIdx.x == 0 && tid == 0) A.prefix[A.n_seqs] = all;
     __syncthreads();
-    if (w0 >= n_w || total == 0) return;
-    const int64_t w = w0 + warp;
-    t0 = w < n_w ? w * total / n_w : total;
-    t1 = w < n_w ? (w + 1) * total / n_w : total;
+    t0 = deal.start(w0 + warp);
+    t1 = deal.start(w0 + warp + 1);
+    if (starts[0] >= total) return;
     if (t0 < t1) {
       cur.s = int(J.at[warp][0]);
       cur.n = clamped(A, cur.s);
       const int64_t tl = tiles_of<KEYS>(cur.n), base = J.at[warp][1] * per;
-      cur.ub = int((t0 - base) / tl);
+      cur.ub = int(quotient(t0 - base, tl));
       cur.first = base + cur.ub * tl;
       cur.end = cur.first + tl;
     }
@@ -757,35 +809,27 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
     const int64_t s = unit / per;
     const int ub = int(unit - s * per), h0 = (ub % A.hb) * HU, heads = min(HU, A.group - h0);
     const int64_t qrow = s * A.hq + int64_t(ub / A.hb) * A.group + h0;
-    for (int i = tid; i < heads * D; i += kThreads) {
+    for (int i = tid * 4; i < heads * D; i += kThreads * 4) {
       const int h = i / D, e = i % D;
-      float M = -INFINITY, L = 0.f, acc = 0.f;
+      float M = -INFINITY, L = 0.f, acc[4] = {};
       for (int w = a; w < b; ++w) M = fmaxf(M, J.m[w][h]);
       for (int w = a; w < b; ++w) {
         const float lw = J.l[w][h], f = lw != 0.f ? ex2(J.m[w][h] - M) : 0.f;
+        const float4 x = *reinterpret_cast<const float4*>(states + (w * HU + h) * D + e);
         L += lw * f;
-        acc += states[(w * HU + h) * D + e] * f;
+        acc[0] += x.x * f; acc[1] += x.y * f; acc[2] += x.z * f; acc[3] += x.w * f;
       }
       if (whole) {
-        store_o(static_cast<Qt*>(A.O) + (qrow + h) * D + e, L == 0.f ? 0.f : acc / L);
+        const float f = L == 0.f ? 0.f : 1.f / L;
+        store4(static_cast<Qt*>(A.O) + (qrow + h) * D + e, acc[0] * f, acc[1] * f, acc[2] * f, acc[3] * f);
         if (e == 0 && A.lse != nullptr) A.lse[qrow + h] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
       } else {
         float* slot = A.slots + ((int64_t(blockIdx.x) * kWarps + a) * HU + h) * (D + 4);
-        slot[4 + e] = acc;
+        store4(slot + 4 + e, acc[0], acc[1], acc[2], acc[3]);
         if (e == 0) { slot[0] = M; slot[1] = L; }
       }
     }
   }
-}
-
-// a / b for quotients below 2^31 and a below 2^53: a quotient in 64-bit floats, then
-// put right (the hardware has no 64-bit integer division).
-__device__ __forceinline__ int quotient(int64_t a, int64_t b) {
-  int64_t q = int64_t(double(a) / double(b));
-  const int64_t r = a - q * b;
-  if (r < 0) --q;
-  if (r >= b) ++q;
-  return int(q);
 }
 
 // A unit's pieces joined: nothing to do for a finished unit; zeros for one without
@@ -794,7 +838,7 @@ __device__ __forceinline__ int quotient(int64_t a, int64_t b) {
 template <typename Qt, int D, int HU>
 __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const BatchArgs A) {
   constexpr int EPL = D / 32, kJoinWarps = kJoinThreads / 32;
-  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool wide = gridDim.y > 1;
   const int split = wide ? kJoinWarps : 1, part = wide ? warp : 0;
@@ -804,61 +848,82 @@ __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const B
   const int heads = min(HU, A.group - (ub % A.hb) * HU);
   const int64_t row0 = int64_t(s) * A.hq + int64_t(ub / A.hb) * A.group + (ub % A.hb) * HU;
   const int64_t seq_tile = A.prefix[s], tl = A.prefix[s + 1] - seq_tile;
-  const int64_t total = A.prefix[A.n_seqs] * per, n_w = A.prefix[A.n_seqs + 1];
+  const int64_t total = A.prefix[A.n_seqs] * per;
   int w0 = 0, w1 = 0, groups = 0, n = 0;
   if (tl > 0) {
     // Warps w0..w1 have the unit; the last one's state is an end piece unless the unit
     // ends with that warp's tiles.
+    const Deal deal(A, total);
     const int64_t lo = seq_tile * per + ub * tl, hi = lo + tl;
-    w0 = quotient((lo + 1) * n_w - 1, total);
-    w1 = quotient(hi * n_w - 1, total);
-    const bool apart = hi != quotient((w1 + 1) * total, n_w);
+    w0 = int(deal.owner(lo));
+    w1 = int(deal.owner(hi - 1));
+    const bool apart = hi != deal.start(w1 + 1);
     groups = w1 - apart < w0 ? 0 : (w1 - apart) / kWarps - w0 / kWarps + 1;
     n = groups + apart;
     if (w0 == w1 || n == 1) return;
   }
   for (int h = wide ? blockIdx.y : warp; h < heads; h += kJoinWarps) {
-    auto slot = [&](int i) {
-      const int64_t at = i < groups ? max(w0, (w0 / kWarps + i) * kWarps) : kMaxWarps + w1;
-      return const_cast<const float*>(A.slots) + (at * HU + h) * (D + 4);
-    };
+    // Pieces in rounds of 8, all of a round's loads before its arithmetic.
     float M = -INFINITY, L = 0.f, acc[EPL] = {};
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = __ldg(reinterpret_cast<const float2*>(slot(i)));
-      if (ml.y != 0.f) M = fmaxf(M, ml.x);
-    }
-    M = warp_max(M);
-#pragma unroll 8
-    for (int i = part; i < n; i += split) {
-      const float* p = slot(i);
-      const float2 ml = __ldg(reinterpret_cast<const float2*>(p));
-      float x[EPL];
-      load_slice<EPL>(p + 4, lane * EPL, x);
-      const float f = ml.y != 0.f ? ex2(ml.x - M) : 0.f;
-      L += ml.y * f;
+    for (int i0 = part; i0 < n; i0 += 8 * split) {
+      float2 ml[8];
+      float x[8][EPL];
+      float top = M;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = f == 0.f ? acc[e] : fmaf(x[e], f, acc[e]);
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * split;
+        ml[k] = make_float2(0.f, 0.f);
+        if (i < n) {
+          const int64_t at = i < groups ? max(w0, (w0 / kWarps + i) * kWarps) : kMaxWarps + w1;
+          const float* p = A.slots + (at * HU + h) * (D + 4);
+          ml[k] = *reinterpret_cast<const float2*>(p);
+          load_slice<EPL>(p + 4, lane * EPL, x[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
+      const float keep = L != 0.f ? ex2(M - top) : 0.f;
+      M = top;
+      L *= keep;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] *= keep;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (ml[k].y != 0.f) {
+          const float f = ex2(ml[k].x - top);
+          L += ml[k].y * f;
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) acc[e] = fmaf(x[k][e], f, acc[e]);
+        }
     }
     if (wide) {
 #pragma unroll
       for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
-      if (lane == 0) s_l[warp] = L;
+      if (lane == 0) { s_m[warp] = M; s_l[warp] = L; }
       __syncthreads();
       if (warp != 0) return;
+      M = -INFINITY;
       L = 0.f;
 #pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) L += s_l[k];
+      for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        acc[e] = 0.f;
+      for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, s_m[k]);
 #pragma unroll
-        for (int k = 0; k < kJoinWarps; ++k) acc[e] += s_o[k][lane * EPL + e];
+      for (int k = 0; k < kJoinWarps; ++k) {
+        const float f = s_l[k] != 0.f ? ex2(s_m[k] - M) : 0.f;
+        L += s_l[k] * f;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] += s_o[k][lane * EPL + e] * f;
       }
     }
+    const float f = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      store_o(static_cast<Qt*>(A.O) + (row0 + h) * D + lane * EPL + e, L == 0.f ? 0.f : acc[e] / L);
+    for (int e = 0; e < EPL; ++e) acc[e] *= f;
+    if constexpr (EPL == 4) store4(static_cast<Qt*>(A.O) + (row0 + h) * D + lane * 4, acc[0], acc[1], acc[2], acc[3]);
+    else
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) store_o(static_cast<Qt*>(A.O) + (row0 + h) * D + lane * EPL + e, acc[e]);
     if (lane == 0 && A.lse != nullptr) A.lse[row0 + h] = L == 0.f ? -INFINITY : 0.69314718056f * (M + log2f(L));
     if (wide) return;
   }
@@ -875,7 +940,11 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   const int64_t units = int64_t(A.n_seqs) * A.hkv * A.hb;
   const int64_t tiles = (A.max_tokens + Tile<Kv, D>::kKeys - 1) / Tile<Kv, D>::kKeys;
   A.single = tiles <= kSingleTiles && units <= int64_t(sms) * 2;
-  const int64_t ctas = A.single ? units : max64(1, min64(min64(int64_t(sms) * 2, kMaxCtas), (units * tiles + kWarps * kMinTiles - 1) / (kWarps * kMinTiles)));
+  sms = sms < kMaxSms ? sms : kMaxSms;
+  const int64_t most = units * tiles;
+  A.first_ctas = int32_t(max64(1, min64(sms * 2, (most + kWarps * kMinTiles - 1) / (kWarps * kMinTiles))));
+  A.ctas = most >= int64_t(kTwoTiers) * kWarps * sms * 2 ? sms * 4 : A.first_ctas;
+  const int64_t ctas = A.single ? units : A.ctas;
   {
     TraceScope ts("attend_batch_kernel", 0, s);
     zha_count_launch();
