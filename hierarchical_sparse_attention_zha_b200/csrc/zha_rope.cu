@@ -9,10 +9,17 @@
 // (unsigned arithmetic, also for negative m), and what is left is exact to
 // m * 2^-54 turns (the table's own rounding). The nearest quarter turn comes off as two
 // bits, so the sine and cosine see an argument of at most an eighth of a turn,
-// rounded at 2^-28 turns.
+// rounded at 2^-28 turns: there their Taylor series to x^9 and x^10 are off by less
+// than 2^-28.
 //
-// Bound: HBM, each row read once and written once.
+// A row is read in pieces of 8 elements, two a lane: the two that hold the elements of
+// 8 pairs, so that a lane turns what it has read. (Half layout with an odd split: two
+// adjacent pieces, and the pairs' other elements once more, one by one.) A block makes
+// the cosines and sines of its tokens once, while its first rows are on their way.
+//
+// Bound: HBM, each row read once and written once; the launch for few tokens.
 #include <cmath>
+#include <type_traits>
 
 #include "zha_host.cuh"
 #include "zha_internal.cuh"
@@ -21,7 +28,10 @@ namespace zha {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeTokens = 32;          // a block, at most
+constexpr int kRopeTarget = 192;
 
 struct RopeTable {
   int32_t pairs;               // 0: nothing is turned
@@ -42,8 +52,9 @@ __device__ __forceinline__ float2 cos_sin_of(uint64_t turn, int64_t pos, float a
   const uint32_t u = uint32_t((turn * uint64_t(pos) + 0x80000000ull) >> 32);   // turns * 2^32
   const uint32_t quarter = (u + 0x20000000u) >> 30;
   const float x = float(int32_t(u - (quarter << 30))) * 0x1p-31f;                // half turns, |x| <= 1/4
-  float s, c;
-  sincospif(x, &s, &c);
+  const float z = x * 3.14159265359f, y = z * z;
+  const float s = fmaf(z * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), z);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
   float co = (quarter & 1u) ? s : c, si = (quarter & 1u) ? c : s;
   if (quarter == 1u || quarter == 2u) co = -co;
   if (quarter == 2u || quarter == 3u) si = -si;
@@ -51,165 +62,276 @@ __device__ __forceinline__ float2 cos_sin_of(uint64_t turn, int64_t pos, float a
   return make_float2(co * amplitude, si * amplitude);
 }
 
-template <int N>
-__device__ __forceinline__ void load_n(const float* p, float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(p + i);
-    v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+// Pieces of 8 elements as they lie in memory.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  uint32_t w[8];
+  __device__ void load(const float* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
-}
-__device__ __forceinline__ void load_n(const __nv_bfloat16* p, float (&v)[8]) { load_slice<8>(p, 0, v); }
-
-__device__ __forceinline__ void store_n(float* p, const float (&v)[8]) {
+  __device__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ void load(const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  }
+  __device__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+__device__ __forceinline__ void store_8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void store_n(__nv_bfloat16* p, const float (&v)[8]) {
+__device__ __forceinline__ void store_8(__nv_bfloat16* p, const float (&v)[8]) {
   uint4 x;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&x);
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
   *reinterpret_cast<uint4*>(p) = x;
 }
-__device__ __forceinline__ float load_1(const float* p) { return *p; }
-__device__ __forceinline__ float load_1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Work units of a row. Every unit owns all the elements it reads, so a row may
-// be turned in place.
-//   interleaved:               d/8 units of 8 elements (4 pairs)
-//   half, pairs % 8 == 0:      pairs/8 units of 8 pairs, then (d - 2 pairs)/8 of
-//                              8 elements that stay
-//   half, other pair counts:   pairs units of one pair, then d - 2 pairs single
-//                              elements (rows are not 16-byte addressable at i + pairs)
-__host__ __device__ inline int row_units(const RopeTable& R, int d) {
-  if (!R.half || R.pairs == 0) return d / 8;
-  return R.pairs % 8 == 0 ? d / 8 - R.pairs / 8 : d - R.pairs;
+// Where the other element of a pair is: beside it, in the lane's other piece, elsewhere.
+enum { kOwn = 0, kPair = 1, kAcross = 2 };
+int mode_of(const RopeTable& R) { return !R.half ? kOwn : R.pairs % 8 == 0 ? kPair : kAcross; }
+
+// Where a token's cosine and sine of pair p lie: so that the lanes of a row, which
+// take two pairs of their 8 at a time, read adjacent 16 bytes.
+template <int MODE>
+__device__ __forceinline__ int turn_slot(int p) {
+  return MODE == kAcross ? p : ((p % 8 / 2) * 8 + p / 8) * 2 + p % 2;
 }
 
-template <typename Src, typename Dst>
-__device__ __forceinline__ void turn_unit(const Src* x, Dst* y, int u, int P, bool half, bool turned,
-                                          const float2* cs) {
-  if (!turned || !half) {
-    float v[8];
-    load_n(x + u * 8, v);
-    if (turned) {
+// What a lane does with its two pieces (from elements a0 and b0 on) of every row.
+template <int D, int MODE>
+struct Lane {
+  int unit, a0, b0;
+  bool on;
+  __device__ Lane(int P, int lane) : unit(lane % (D / 16)) {
+    const bool pair = MODE == kPair && unit < P / 8;          // the others copy the pieces behind the pairs
+    a0 = pair ? unit * 8 : unit * 16;
+    b0 = pair ? a0 + P : a0 + 8;
+    on = MODE == kPair ? pair : MODE == kOwn ? unit * 8 < P : a0 < 2 * P;
+  }
+
+  // The pieces a and b of a row, turned. For kAcross elements are read once more.
+  template <typename T>
+  __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* cs, const T* row, int P) const {
+    const float4* two = reinterpret_cast<const float4*>(cs);
+    if constexpr (MODE == kPair) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (u * 4 + i < P) {
-          const float2 t = cs[u * 4 + i];
-          const float a = v[2 * i], b = v[2 * i + 1];
-          v[2 * i] = a * t.x - b * t.y;
-          v[2 * i + 1] = a * t.y + b * t.x;
+      for (int j = 0; j < 4; ++j) {
+        const float4 t = two[j * 8 + unit];
+        const float a0 = a[2 * j], a1 = a[2 * j + 1], b0 = b[2 * j], b1 = b[2 * j + 1];
+        a[2 * j] = a0 * t.x - b0 * t.y;
+        b[2 * j] = a0 * t.y + b0 * t.x;
+        a[2 * j + 1] = a1 * t.z - b1 * t.w;
+        b[2 * j + 1] = a1 * t.w + b1 * t.z;
+      }
+    } else if constexpr (MODE == kOwn) {
+      const int left = P - unit * 8;                          // pairs of the lane's 8 that turn
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 t = two[j * 8 + unit];
+        float* v = j < 2 ? a + 4 * j : b + 4 * (j - 2);
+        const float v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+        if (2 * j < left) {
+          v[0] = v0 * t.x - v1 * t.y;
+          v[1] = v0 * t.y + v1 * t.x;
+        }
+        if (2 * j + 1 < left) {
+          v[2] = v2 * t.z - v3 * t.w;
+          v[3] = v2 * t.w + v3 * t.z;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int e = a0 + i;
+        if (e >= 2 * P) break;
+        float& v = i < 8 ? a[i & 7] : b[i & 7];
+        const float2 t = cs[e < P ? e : e - P];
+        v = v * t.x + float(row[e < P ? e + P : e - P]) * (e < P ? -t.y : t.y);
+      }
+    }
+  }
+};
+
+// The shape of a block's work. Its warps read `slots` rows at a time (with the blocks
+// in y); a lane keeps its row's number, and goes from token to token: every
+// `abreast`-th, where that many tokens' rows fit in the slots.
+struct RowPlan {
+  int tokens, rows, abreast;
+};
+
+// One kind of row of one token.
+template <typename Src>
+struct Row {
+  const Src* at;
+  int64_t token;                                             // stride
+};
+
+// Calls store(row, element, values, to) with the pieces of all rows of `have` tokens.
+// where(row) gives the place of the first token's row, and target(token, row) the
+// destination `to`, asked for a batch at a time; rows from `plain` on are not turned.
+// ready() runs while the first batch is on its way, and ends with the block in step.
+template <int D, int MODE, typename Src, typename Where, typename Ready, typename Target, typename Store>
+__device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const float2 (*cs)[64], int P, int plain,
+                                          Where where, Ready ready, Target target, Store store) {
+  constexpr int kPer = 512 / D;                               // rows a warp reads at a time
+  constexpr int kRows = 2;                                    // a lane has in flight
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Lane<D, MODE> mine(P, lane);
+  const int slots = kRopeWarps * kPer * int(gridDim.y);
+  const int slot = (int(blockIdx.y) * kRopeWarps + warp) * kPer + lane / (D / 16);
+  const int t_first = plan.abreast > 1 ? slot / plan.rows : 0;
+  const bool idle = t_first >= plan.abreast;
+  bool begun = false;
+  for (int pass = 0; pass < plan.rows; pass += slots) {
+    const int r = slot - t_first * plan.rows + pass;
+    const bool there = r < plan.rows && !idle, turned = mine.on && r < plain;
+    const Row<Src> row = where(there ? r : 0);
+    for (int t0 = 0; t0 < have; t0 += plan.abreast * kRows) {
+      Piece<Src> x[kRows], y[kRows];
+      int64_t to[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int t = t0 + t_first + k * plan.abreast;
+        if (there && t < have) {
+          x[k].load(row.at + t * row.token + mine.a0);
+          y[k].load(row.at + t * row.token + mine.b0);
+        }
+      }
+      if (!begun) ready();
+      begun = true;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int t = t0 + t_first + k * plan.abreast;
+        to[k] = there && t < have ? target(t, r) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (t0 + k * plan.abreast >= have) break;
+        const int t = t0 + t_first + k * plan.abreast;
+        const bool here = there && t < have;
+        float a[8], b[8];
+        x[k].get(a);
+        y[k].get(b);
+        if (here && turned) mine.turn(a, b, cs[t], row.at + t * row.token, P);
+        if (MODE == kAcross) __syncwarp();                   // a row in place is read before it is written
+        if (here) {
+          store(r, mine.a0, a, to[k]);
+          store(r, mine.b0, b, to[k]);
         }
       }
     }
-    store_n(y + u * 8, v);
-    return;
-  }
-  if (P % 8 == 0) {
-    if (u < P / 8) {
-      float a[8], b[8];
-      load_n(x + u * 8, a);
-      load_n(x + P + u * 8, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 t = cs[u * 8 + i];
-        const float p = a[i], q = b[i];
-        a[i] = p * t.x - q * t.y;
-        b[i] = p * t.y + q * t.x;
-      }
-      store_n(y + u * 8, a);
-      store_n(y + P + u * 8, b);
-    } else {
-      float v[8];
-      load_n(x + P + u * 8, v);
-      store_n(y + P + u * 8, v);
-    }
-    return;
-  }
-  if (u < P) {
-    const float2 t = cs[u];
-    const float a = load_1(x + u), b = load_1(x + P + u);
-    store_1(y + u, a * t.x - b * t.y);
-    store_1(y + P + u, a * t.y + b * t.x);
-  } else {
-    store_1(y + P + u, load_1(x + P + u));
   }
 }
 
-// Units of a row that is only copied: d/8.
-template <typename Src, typename Dst>
-__device__ __forceinline__ void turn_row_unit(const void* src, int64_t so, void* dst, int64_t d_o, int u,
-                                              const RopeTable& R, bool turned, const float2* cs) {
-  turn_unit(static_cast<const Src*>(src) + so, static_cast<Dst*>(dst) + d_o, u, R.pairs, R.half != 0, turned, cs);
+// Cosines and sines of `have` tokens from t0 on.
+template <int MODE>
+__device__ __forceinline__ void fill_turns(const RopeTable& R, float2 (*cs)[64], const int64_t* pos, int have, bool back) {
+  for (int i = threadIdx.x; i < have * 64; i += kRopeThreads)
+    if (i % 64 < R.pairs) cs[i / 64][turn_slot<MODE>(i % 64)] = cos_sin_of(R.turn[i % 64], pos[i / 64], R.amplitude, back);
 }
 
-template <typename Src, typename Dst>
-__global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_constant__ RopeTable R, RowSet X,
-                                                                  const int64_t* pos, int64_t n_tokens, int d,
-                                                                  int back) {
-  __shared__ float2 cs[64];
+// Blocks in x take `plan.tokens` tokens each, blocks in y share out their rows.
+template <typename Src, typename Dst, int D, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(Src) == 2 ? 4 : 3)
+    rope_apply_kernel(const __grid_constant__ RopeTable R, RowSet X, const int64_t* pos, int64_t n_tokens, RowPlan plan,
+                      int back) {
+  __shared__ __align__(16) float2 cs[kRopeTokens][64];
   pdl_trigger();
   pdl_wait();
-  const int units = row_units(R, d), total = X.heads * units;
-  for (int64_t t = blockIdx.x; t < n_tokens; t += gridDim.x) {
-    if (threadIdx.x < R.pairs) cs[threadIdx.x] = cos_sin_of(R.turn[threadIdx.x], pos[t], R.amplitude, back != 0);
-    __syncthreads();
-    for (int i = threadIdx.x + blockIdx.y * kRopeThreads; i < total; i += kRopeThreads * gridDim.y) {
-      const int h = i / units, u = i - h * units;
-      turn_row_unit<Src, Dst>(X.src, t * X.src_token + h * X.src_head, X.dst, t * X.dst_token + h * X.dst_head, u,
-                              R, true, cs);
-    }
-    __syncthreads();
+  for (int64_t t0 = int64_t(blockIdx.x) * plan.tokens; t0 < n_tokens; t0 += int64_t(gridDim.x) * plan.tokens) {
+    const int have = int(min64(plan.tokens, n_tokens - t0));
+    const Src* src = static_cast<const Src*>(X.src) + t0 * X.src_token;
+    Dst* dst = static_cast<Dst*>(X.dst) + t0 * X.dst_token;
+    turn_rows<D, MODE, Src>(
+        plan, have, cs, R.pairs, X.heads, [&](int r) { return Row<Src>{src + r * X.src_head, X.src_token}; },
+        [&] {
+          __syncthreads();
+          fill_turns<MODE>(R, cs, pos + t0, have, back != 0);
+          __syncthreads();
+        },
+        [&](int t, int r) { return t * X.dst_token + r * X.dst_head; },
+        [&](int, int e, const float (&v)[8], int64_t to) { store_8(dst + to + e, v); });
   }
 }
 
-template <typename Src, typename Kv, typename Qo>
-__global__ void __launch_bounds__(kRopeThreads)
+template <typename Src, typename Kv, typename Qo, int D, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(Src) == 2 ? 4 : 3)
     rope_append_kernel(const __grid_constant__ RopeTable R, RowSet Q, RowSet K, RowSet V, KvView kv, int n_seqs,
-                       const int32_t* seq, const int64_t* index, const int64_t* pos, int64_t n_new, int d, int chunk,
+                       const int32_t* seq, const int64_t* index, const int64_t* pos, int64_t n_new, RowPlan plan, int chunk,
                        int32_t* status) {
-  __shared__ float2 cs[64];
+  __shared__ __align__(16) float2 cs[kRopeTokens][64];
+  // Of each token, for its first KV head (-1: nothing is written): the table's entry
+  // and the place in the page; in a contiguous cache the row.
+  __shared__ int64_t s_at[kRopeTokens];
+  __shared__ int32_t s_in[kRopeTokens];
   pdl_trigger();
   pdl_wait();
-  const int hkv = K.heads;
-  const int units = row_units(R, d), vunits = d / 8;
-  const int nq = Q.heads * units, nk = hkv * units, total = nq + nk + hkv * vunits;
+  const int hq = Q.heads, hkv = K.heads;
   const int64_t limit = kv.table == nullptr ? kv.ld : kv.max_blocks * chunk;
-  for (int64_t t = blockIdx.x; t < n_new; t += gridDim.x) {
-    const int32_t s = seq[t];
-    if (s < 0) continue;                              // the whole block agrees
-    const int64_t at = index[t];
-    if (s >= n_seqs || at < 0 || at >= limit) {
-      if (threadIdx.x == 0 && blockIdx.y == 0 && status != nullptr) atomicOr(status, ZHA_DEV_BAD_SEQUENCE);
-      continue;
-    }
-    if (threadIdx.x < R.pairs)
-      cs[threadIdx.x] = cos_sin_of(R.turn[threadIdx.x], pos != nullptr ? pos[t] : at, R.amplitude, false);
-    __syncthreads();
-    for (int i = threadIdx.x + blockIdx.y * kRopeThreads; i < total; i += kRopeThreads * gridDim.y) {
-      if (i < nq) {
-        const int h = i / units, u = i - h * units;
-        turn_row_unit<Src, Qo>(Q.src, t * Q.src_token + h * Q.src_head, Q.dst, t * Q.dst_token + int64_t(h) * d, u, R,
-                               R.pairs > 0, cs);
-        continue;
-      }
-      const bool key = i < nq + nk;
-      const int j = key ? i - nq : i - nq - nk, per = key ? units : vunits;
-      const int g = j / per, u = j - g * per;
-      const int32_t row = kv_batch_row(kv, hkv, s, g, at, chunk);
-      if (row < 0) {
-        if (status != nullptr) atomicOr(status, ZHA_DEV_BAD_PAGE);
-        continue;
-      }
-      const RowSet& S = key ? K : V;
-      turn_row_unit<Src, Kv>(S.src, t * S.src_token + g * S.src_head, S.dst, int64_t(row) * d, u, R,
-                             key && R.pairs > 0, cs);
-    }
-    __syncthreads();
+  for (int64_t t0 = int64_t(blockIdx.x) * plan.tokens; t0 < n_new; t0 += int64_t(gridDim.x) * plan.tokens) {
+    const int have = int(min64(plan.tokens, n_new - t0));
+    const Src* q = static_cast<const Src*>(Q.src) + t0 * Q.src_token;
+    const Src* k = static_cast<const Src*>(K.src) + t0 * K.src_token;
+    const Src* v = static_cast<const Src*>(V.src) + t0 * V.src_token;
+    turn_rows<D, MODE, Src>(
+        plan, have, cs, R.pairs, R.pairs > 0 ? hq + hkv : 0,
+        [&](int r) {
+          return r < hq         ? Row<Src>{q + r * Q.src_head, Q.src_token}
+                 : r < hq + hkv ? Row<Src>{k + (r - hq) * K.src_head, K.src_token}
+                                : Row<Src>{v + (r - hq - hkv) * V.src_head, V.src_token};
+        },
+        [&] {
+          __syncthreads();
+          if (threadIdx.x < have) {
+            const int t = threadIdx.x;
+            const int32_t s = seq[t0 + t];
+            const int64_t at = index[t0 + t];
+            const bool fits = s < n_seqs && at >= 0 && at < limit;
+            if (s >= 0 && !fits && status != nullptr && blockIdx.y == 0) atomicOr(status, ZHA_DEV_BAD_SEQUENCE);
+            const int block = kv.table == nullptr || !fits ? 0 : int(at >> 32 ? at / chunk : uint32_t(at) / uint32_t(chunk));
+            const int64_t head = int64_t(s) * hkv;
+            s_at[t] = s < 0 || !fits ? -1 : kv.table == nullptr ? head * kv.ld + at : head * kv.max_blocks + block;
+            s_in[t] = int(at - int64_t(block) * chunk);
+          }
+          fill_turns<MODE>(R, cs, (pos != nullptr ? pos : index) + t0, have, false);
+          __syncthreads();
+        },
+        // the row in q_out or in the cache, -1: none
+        [&](int t, int r) -> int64_t {
+          const int64_t at = s_at[t];
+          if (at < 0) return -1;
+          if (r < hq) return (t0 + t) * hq + r;
+          const int g = r < hq + hkv ? r - hq : r - hq - hkv;
+          if (kv.table == nullptr) return at + g * kv.ld;
+          const int32_t page = kv.table[at + g * kv.max_blocks];
+          if (page >= 0 && page < kv.ld) return int64_t(page) * chunk + s_in[t];
+          if (status != nullptr) atomicOr(status, ZHA_DEV_BAD_PAGE);
+          return -1;
+        },
+        [&](int r, int e, const float (&x)[8], int64_t to) {
+          if (to < 0) return;
+          if (r < hq) store_8(static_cast<Qo*>(Q.dst) + to * D + e, x);
+          else store_8(static_cast<Kv*>(r < hq + hkv ? K.dst : V.dst) + to * D + e, x);
+        });
   }
 }
 
@@ -223,12 +345,25 @@ RopeTable table_of(const zha_rope* r) {
   return t;
 }
 
-// One block per token; few tokens with many units are spread over blocks in y.
-dim3 rope_grid(int64_t tokens, int64_t units) {
-  const int64_t x = tokens < (1 << 20) ? tokens : (1 << 20);
-  int64_t y = (units + kRopeThreads - 1) / kRopeThreads;
-  if (x * y > 148 * 16) y = (148 * 16 + x - 1) / x;
-  return dim3(unsigned(x), unsigned(y < 1 ? 1 : y > 65535 ? 65535 : y));
+// Tokens a block: enough for kRopeTarget rows of 128 elements (the turns and the
+// block's start are paid once), but none idle while another has two.
+// Few tokens have their rows spread over blocks in y.
+struct RopeGrid {
+  dim3 grid;
+  RowPlan plan;
+};
+RopeGrid rope_grid(int64_t n, int64_t rows, int d, int sms) {
+  RopeGrid g;
+  const int64_t target = int64_t(kRopeTarget) * 128 / d, at_once = kRopeWarps * (512 / d);
+  int64_t tokens = min64(kRopeTokens, round_up((target + rows - 1) / rows, 2));
+  tokens = max64(1, min64(tokens, n / (int64_t(sms) * 2)));
+  const int64_t x = (n + tokens - 1) / tokens;
+  const int64_t y = max64(1, min64((tokens * rows + at_once - 1) / at_once, int64_t(sms) * 8 / x));
+  g.grid = dim3(unsigned(min64(x, 1 << 20)), unsigned(min64(y, 65535)));
+  g.plan.tokens = int(tokens);
+  g.plan.rows = int(rows);
+  g.plan.abreast = int(max64(1, min64(tokens, at_once * g.grid.y / rows)));
+  return g;
 }
 
 bool rope_ok(const zha_rope* r) {
@@ -258,24 +393,40 @@ bool rows_apart(const zha_rows* r, int64_t tokens, int64_t heads, int64_t d) {
   return h <= t ? h >= d && (t - d) / h >= heads - 1 : t >= d && (h - d) / t >= tokens - 1;
 }
 
-template <typename Src, typename Dst>
-cudaError_t launch_apply(const RopeTable& R, const RowSet& X, const int64_t* pos, int64_t n, int d, int back,
+template <typename Src, typename Dst, int D, int MODE>
+cudaError_t launch_apply(const RopeTable& R, const RowSet& X, const int64_t* pos, int64_t n, int back, const RopeGrid& g,
                          cudaStream_t s) {
   TraceScope ts("rope_apply_kernel", 0, s);
   zha_count_launch();
-  return launch_pdl(rope_apply_kernel<Src, Dst>, rope_grid(n, int64_t(X.heads) * row_units(R, d)),
-                    dim3(kRopeThreads), 0, s, R, X, pos, n, d, back);
+  return launch_pdl(rope_apply_kernel<Src, Dst, D, MODE>, g.grid, dim3(kRopeThreads), 0, s, R, X, pos, n, g.plan, back);
 }
 
-template <typename Src, typename Kv, typename Qo>
+template <typename Src, typename Kv, typename Qo, int D, int MODE>
 cudaError_t launch_append(const RopeTable& R, const RowSet& Q, const RowSet& K, const RowSet& V, const KvView& kv,
-                          int n_seqs, const int32_t* seq, const int64_t* index, const int64_t* pos, int64_t n,
-                          int d, int chunk, int32_t* status, cudaStream_t s) {
+                          int n_seqs, const int32_t* seq, const int64_t* index, const int64_t* pos, int64_t n, int chunk,
+                          int32_t* status, const RopeGrid& g, cudaStream_t s) {
   TraceScope ts("rope_append_kernel", 0, s);
   zha_count_launch();
-  const int64_t units = int64_t(Q.heads + K.heads) * row_units(R, d) + int64_t(V.heads) * (d / 8);
-  return launch_pdl(rope_append_kernel<Src, Kv, Qo>, rope_grid(n, units), dim3(kRopeThreads), 0, s, R, Q, K, V, kv,
-                    n_seqs, seq, index, pos, n, d, chunk, status);
+  return launch_pdl(rope_append_kernel<Src, Kv, Qo, D, MODE>, g.grid, dim3(kRopeThreads), 0, s, R, Q, K, V, kv, n_seqs, seq,
+                    index, pos, n, g.plan, chunk, status);
+}
+
+// f(head dimension, mode) with both as types.
+template <typename F>
+cudaError_t with_shape(int d, int mode, F f) {
+  using std::integral_constant;
+  auto by_mode = [&](auto dim) {
+    switch (mode) {
+      case kOwn: return f(dim, integral_constant<int, kOwn>());
+      case kPair: return f(dim, integral_constant<int, kPair>());
+      default: return f(dim, integral_constant<int, kAcross>());
+    }
+  };
+  return d == 128 ? by_mode(integral_constant<int, 128>()) : by_mode(integral_constant<int, 64>());
+}
+template <typename F>
+cudaError_t with_type(int32_t dtype, F f) {
+  return dtype == ZHA_F32 ? f(float()) : f(__nv_bfloat16());
 }
 
 }  // namespace
@@ -372,13 +523,17 @@ zha_status zha_rope_apply(const zha_rope* rope, const zha_rows* x, int32_t x_dty
            n_heads};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int d = rope->head_dim, back = inverse != 0;
-  using bf = __nv_bfloat16;
-  cudaError_t e =
-      x_dtype == ZHA_F32
-          ? (y_dtype == ZHA_F32 ? zha::launch_apply<float, float>(R, X, d_pos, n_tokens, d, back, s)
-                                : zha::launch_apply<float, bf>(R, X, d_pos, n_tokens, d, back, s))
-          : (y_dtype == ZHA_F32 ? zha::launch_apply<bf, float>(R, X, d_pos, n_tokens, d, back, s)
-                                : zha::launch_apply<bf, bf>(R, X, d_pos, n_tokens, d, back, s));
+  int sms = 0;
+  cudaError_t e = zha::device_sm_count(&sms);
+  if (e != cudaSuccess) return zha_report_cuda(e, "zha_rope_apply");
+  const zha::RopeGrid g = zha::rope_grid(n_tokens, n_heads, d, sms);
+  e = zha::with_shape(d, zha::mode_of(R), [&](auto dim, auto mode) {
+    return zha::with_type(x_dtype, [&](auto src) {
+      return zha::with_type(y_dtype, [&](auto dst) {
+        return zha::launch_apply<decltype(src), decltype(dst), dim.value, mode.value>(R, X, d_pos, n_tokens, back, g, s);
+      });
+    });
+  });
   return e == cudaSuccess ? ZHA_OK : zha_report_cuda(e, "zha_rope_apply");
 }
 
@@ -413,22 +568,20 @@ zha_status zha_rope_append_kv(const zha_config* cfg, const zha_rope* rope, const
   K = RowSet{k->data, const_cast<void*>(kv->k), k->token_stride, k->head_stride, 0, 0, G.hkv};
   V = RowSet{v->data, const_cast<void*>(kv->v), v->token_stride, v->head_stride, 0, 0, G.hkv};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  using bf = __nv_bfloat16;
-  auto go = [&](auto launch) {
-    return launch(R, Q, K, V, view, n_seqs, d_seq, d_index, d_pos, n_new, G.d, G.chunk, d_status, s);
-  };
-  const int which = (src_dtype == ZHA_BF16 ? 4 : 0) + (G.kv_bf16 ? 2 : 0) + (q_dtype == ZHA_BF16 ? 1 : 0);
-  cudaError_t e = cudaSuccess;
-  switch (which) {
-    case 0: e = go(zha::launch_append<float, float, float>); break;
-    case 1: e = go(zha::launch_append<float, float, bf>); break;
-    case 2: e = go(zha::launch_append<float, bf, float>); break;
-    case 3: e = go(zha::launch_append<float, bf, bf>); break;
-    case 4: e = go(zha::launch_append<bf, float, float>); break;
-    case 5: e = go(zha::launch_append<bf, float, bf>); break;
-    case 6: e = go(zha::launch_append<bf, bf, float>); break;
-    default: e = go(zha::launch_append<bf, bf, bf>); break;
-  }
+  int sms = 0;
+  cudaError_t e = zha::device_sm_count(&sms);
+  if (e != cudaSuccess) return zha_report_cuda(e, who);
+  const zha::RopeGrid g = zha::rope_grid(n_new, int64_t(Q.heads) + 2 * G.hkv, G.d, sms);
+  e = zha::with_shape(G.d, zha::mode_of(R), [&](auto dim, auto mode) {
+    return zha::with_type(src_dtype, [&](auto src) {
+      return zha::with_type(G.kv_bf16 ? ZHA_BF16 : ZHA_F32, [&](auto cache) {
+        return zha::with_type(q_dtype, [&](auto out) {
+          return zha::launch_append<decltype(src), decltype(cache), decltype(out), dim.value, mode.value>(
+              R, Q, K, V, view, n_seqs, d_seq, d_index, d_pos, n_new, G.chunk, d_status, g, s);
+        });
+      });
+    });
+  });
   return e == cudaSuccess ? ZHA_OK : zha_report_cuda(e, who);
 }
 
