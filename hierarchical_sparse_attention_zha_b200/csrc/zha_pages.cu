@@ -6,10 +6,10 @@
 // ranks are prefix sums, so that no atomic's order shows in a result. They want a few
 // passes over the counts with all of a pass done before the next, so one cluster of
 // up to 16 CTAs does them in one launch, with a cluster barrier between passes:
-//   1  how many pages are free (in use, for compact) in each CTA's share of the counts
-//   2  the shares' prefix turns every free page into list[rank]
-//   3  each (item, KV head): is it valid, how many pages does it need
-//   4  the needs' prefix, then entries and counts, with every rank known
+//   1  how many pages are free (in use, for compact) in each CTA's share of the
+//      counts; each (item, KV head): is it valid, how many pages does it need
+//   2  the shares' prefix turns every free page into list[rank]; the needs' prefix
+//   3  entries and counts, with every rank known
 // What moves page contents is wide: a second launch over the whole GPU, unless it is
 // small enough to be done by the cluster.
 // Bound: the launch and the passes' latencies; the copied rows (HBM) for compact.
@@ -25,7 +25,6 @@ namespace {
 constexpr int kPageThreads = 256;         // of the kernels over the whole GPU
 constexpr int kBookThreads = 1024;        // of the cluster's CTAs
 constexpr int kBookWarps = kBookThreads / 32;
-constexpr int kPerThread = 4;             // counts a thread ranks in one go
 constexpr int kMostCtas = 16;
 constexpr int64_t kCopyHere = 256 << 10;  // bytes the cluster copies itself
 
@@ -39,22 +38,20 @@ struct PoolArgs {
   int32_t* status;
 };
 
-// Workspace, int32: scal[8] (total free or live, moves), seg[16], first[n_seqs]
-// (the first item that lists a sequence), need, offs and copy[items * hkv],
-// list[n_pages], code[n_pages] (compact).
+// Workspace, int32: scal[8] (total live, moves), seg[16], need, offs and copy[items *
+// hkv], list[n_pages], code[n_pages] (compact).
 struct PageWs {
-  int32_t *scal, *seg, *first, *need, *offs, *copy, *list, *code;
+  int32_t *scal, *seg, *need, *offs, *copy, *list, *code;
   int64_t bytes;
 };
 
-PageWs page_ws(void* base, int64_t n_pages, int64_t n_seqs, int64_t rows) {
+PageWs page_ws(void* base, int64_t n_pages, int64_t rows) {
   int32_t* p = static_cast<int32_t*>(base);
   PageWs w{};
   int64_t at = 0;
   auto take = [&](int64_t n) { int32_t* q = base == nullptr ? nullptr : p + at; at += round_up(n, 64); return q; };
   w.scal = take(8);
   w.seg = take(kMostCtas);
-  w.first = take(n_seqs);
   w.need = take(rows);
   w.offs = take(rows);
   w.copy = take(rows);
@@ -107,51 +104,72 @@ __device__ I block_prefix(I v, I* s_red, I* sum) {
 
 __device__ __forceinline__ bool counted(int32_t refs, bool live) { return live ? refs > 0 : refs == 0; }
 
+// a / b; 32-bit divisions take a fifth of the 64-bit ones.
+__device__ __forceinline__ int64_t quotient(int64_t a, int32_t b) {
+  return (a >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
+// This CTA's share of n things (n < 2^30), in fours.
 struct Share {
-  int64_t p0, p1;
-};
-__device__ __forceinline__ Share share_of(int64_t n) {
-  return {int64_t(cluster_rank()) * n / gridDim.x, (int64_t(cluster_rank()) + 1) * n / gridDim.x};
-}
-
-// Pass 1: this CTA's share of the counts.
-__device__ void count_share(const PoolArgs& P, const PageWs& W, bool live, int* s_red) {
-  const Share h = share_of(P.n_pages);
-  int n = 0, sum;
-#pragma unroll 4
-  for (int64_t p = h.p0 + threadIdx.x; p < h.p1; p += kBookThreads) n += counted(P.refs[p], live);
-  block_prefix(n, s_red, &sum);
-  if (threadIdx.x == 0) W.seg[cluster_rank()] = sum;
-}
-
-// Pass 2: f(page, counted, exclusive rank) for the share's pages; returns the total.
-template <typename F>
-__device__ int rank_share(const PoolArgs& P, const PageWs& W, bool live, int* s_red, F f) {
-  const Share h = share_of(P.n_pages);
-  int base = 0, total = 0;
-  for (int i = 0; i < int(gridDim.x); ++i) {
-    const int v = __ldcg(W.seg + i);
-    if (i < int(cluster_rank())) base += v;
-    total += v;
+  int a, b;
+  __device__ explicit Share(int n) {
+    const int per = (n + int(gridDim.x) * 4 - 1) / (int(gridDim.x) * 4) * 4;
+    a = min(n, int(cluster_rank()) * per);
+    b = min(n, a + per);
   }
-  for (int64_t q = h.p0; q < h.p1; q += kBookThreads * kPerThread) {
-    const int64_t p = q + threadIdx.x * kPerThread;
-    int n = 0, sum;
-    uint32_t bits = 0;
+};
+
+// Which of the pages p..p + 3 below `end` count, as bits.
+__device__ __forceinline__ uint32_t counted_bits(const int32_t* refs, int p, int end, bool live) {
+  uint32_t bits = 0;
+  if (p + 4 <= end && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+    const int4 r = *reinterpret_cast<const int4*>(refs + p);
+    bits = uint32_t(counted(r.x, live)) | uint32_t(counted(r.y, live)) << 1 | uint32_t(counted(r.z, live)) << 2 |
+           uint32_t(counted(r.w, live)) << 3;
+  } else {
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if (p + i < h.p1 && counted(P.refs[p + i], live)) { bits |= 1u << i; ++n; }
-    int rank = base + block_prefix(n, s_red, &sum);
+    for (int i = 0; i < 4; ++i)
+      if (p + i < end && counted(refs[p + i], live)) bits |= 1u << i;
+  }
+  return bits;
+}
+
+// Pass 1: this thread's part of the share's count. `bits` keeps the share's first
+// 4096 pages' for pass 2.
+__device__ int count_share(const PoolArgs& P, const Share& h, bool live, uint32_t* bits) {
+  *bits = counted_bits(P.refs, h.a + int(threadIdx.x) * 4, h.b, live);
+  int n = __popc(*bits);
+#pragma unroll 4
+  for (int p = h.a + (int(threadIdx.x) + kBookThreads) * 4; p < h.b; p += kBookThreads * 4)
+    n += __popc(counted_bits(P.refs, p, h.b, live));
+  return n;
+}
+
+// The sum of the CTAs' counts, and of those before this one.
+__device__ int2 counts_of(const PageWs& W) {
+  const int lane = threadIdx.x % 32;
+  const int v = lane < int(gridDim.x) ? __ldcg(W.seg + lane) : 0;
+  return make_int2(__reduce_add_sync(0xffffffffu, v),
+                   __reduce_add_sync(0xffffffffu, lane < int(cluster_rank()) ? v : 0));
+}
+
+// Pass 2: f(page, counted, exclusive rank) for the share's pages.
+template <typename F>
+__device__ void rank_share(const PoolArgs& P, const Share& h, bool live, uint32_t bits, int base, int* s_red, F f) {
+  for (int q = h.a; q < h.b; q += kBookThreads * 4) {
+    const int p = q + int(threadIdx.x) * 4;
+    if (q > h.a) bits = counted_bits(P.refs, p, h.b, live);
+    int sum;
+    int rank = base + block_prefix(int(__popc(bits)), s_red, &sum);
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      if (p + i >= h.p1) break;
+    for (int i = 0; i < 4; ++i) {
+      if (p + i >= h.b) break;
       const bool c = (bits >> i) & 1u;
       f(p + i, c, rank);
       rank += c;
     }
     base += sum;
   }
-  return total;
 }
 
 __device__ __forceinline__ void copy_bytes(char* to, const char* from, int64_t n, int id, int step) {
@@ -167,22 +185,28 @@ __device__ __forceinline__ void copy_rows(const PoolArgs& P, int32_t to, int32_t
 }
 
 // ---- extend and fork ----------------------------------------------------------
-// Pass 3, one warp: how many pages row (item, head) needs, -1: refused.
+// One warp: how many pages row (item, head) needs, -1: refused. `list`: the sequences
+// that the call changes.
 template <bool kFork>
-__device__ int row_need(const PoolArgs& P, const PageWs& W, const int32_t* src, const int32_t* dst,
-                        const int64_t* tokens, int item, int g, int lane) {
-  const int32_t d = dst[item], s = kFork ? src[item] : d;
+__device__ int row_need(const PoolArgs& P, const int32_t* src, const int32_t* list, const int64_t* tokens, int n_items,
+                        int item, int g, int lane) {
+  const int32_t d = list[item], s = kFork ? src[item] : d;
   const int64_t n = tokens[item];
+  bool twice = false;
+  for (int j = lane; j < (kFork ? n_items : item); j += 32) {
+    const int32_t x = list[j];
+    twice |= (j < item && x == d) || (kFork && x == s);
+  }
+  twice = __any_sync(0xffffffffu, twice);
   int bad = 0;
-  if (d < 0 || d >= P.n_seqs || s < 0 || s >= P.n_seqs) bad = ZHA_DEV_BAD_SEQUENCE;
-  else if (__ldcg(W.first + d) != item || (kFork && __ldcg(W.first + s) != INT32_MAX)) bad = ZHA_DEV_BAD_SEQUENCE;
+  if (d < 0 || d >= P.n_seqs || s < 0 || s >= P.n_seqs || twice) bad = ZHA_DEV_BAD_SEQUENCE;
   else if (n < 0 || n > P.max_blocks * P.chunk) bad = ZHA_DEV_BAD_LENGTH;
   int need = 0;
   if (bad == 0) {
-    const int64_t blocks = (n + P.chunk - 1) / P.chunk;
+    const int64_t full = quotient(n, P.chunk), blocks = full + (full * P.chunk != n);
     const int32_t* row = P.table + (int64_t(s) * P.hkv + g) * P.max_blocks;
     int miss = 0;
-    bool wrong = false, full = false;
+    bool wrong = false, taken = false;
 #pragma unroll 4
     for (int64_t b = lane; b < blocks; b += 32) {
       const int32_t e = row[b];
@@ -192,15 +216,15 @@ __device__ int row_need(const PoolArgs& P, const PageWs& W, const int32_t* src, 
     if (kFork) {
       const int32_t* to = P.table + (int64_t(d) * P.hkv + g) * P.max_blocks;
 #pragma unroll 4
-      for (int64_t b = lane; b < P.max_blocks; b += 32) full |= to[b] >= 0;
+      for (int64_t b = lane; b < P.max_blocks; b += 32) taken |= to[b] >= 0;
     }
     miss = __reduce_add_sync(0xffffffffu, miss);
     wrong = __any_sync(0xffffffffu, wrong);
-    full = __any_sync(0xffffffffu, full);
+    taken = __any_sync(0xffffffffu, taken);
     if (kFork) {
-      if (full) bad = ZHA_DEV_BAD_SEQUENCE;
+      if (taken) bad = ZHA_DEV_BAD_SEQUENCE;
       else if (wrong || miss) bad = ZHA_DEV_BAD_PAGE;
-      need = n % P.chunk != 0;
+      need = blocks != full;
     } else {
       if (wrong) bad = ZHA_DEV_BAD_PAGE;
       need = miss;
@@ -210,15 +234,14 @@ __device__ int row_need(const PoolArgs& P, const PageWs& W, const int32_t* src, 
   return bad ? -1 : need;
 }
 
-// Pass 4, one warp: the pages list[at], ... go to row (item, head).
+// One warp: the pages list[at], ... go to row (item, head) = idx.
 template <bool kFork>
-__device__ void fill_row(const PoolArgs& P, const PageWs& W, const int32_t* src, const int32_t* dst,
-                         const int64_t* tokens, int64_t idx, int at, bool copy_here, int lane) {
-  const int item = int(idx / P.hkv), g = int(idx % P.hkv);
-  const int64_t n = tokens[item];
-  int32_t* row = P.table + (int64_t(dst[item]) * P.hkv + g) * P.max_blocks;
+__device__ void fill_row(const PoolArgs& P, const PageWs& W, const int32_t* src, int32_t dst, int64_t n, int item, int g,
+                         int idx, int at, bool copy_here, int lane) {
+  int32_t* row = P.table + (int64_t(dst) * P.hkv + g) * P.max_blocks;
+  const int64_t full = quotient(n, P.chunk), rest = n - full * P.chunk;
   if (!kFork) {
-    const int64_t blocks = (n + P.chunk - 1) / P.chunk;
+    const int64_t blocks = full + (rest != 0);
 #pragma unroll 2
     for (int64_t b0 = 0; b0 < blocks; b0 += 32) {
       const int64_t b = b0 + lane;
@@ -233,7 +256,6 @@ __device__ void fill_row(const PoolArgs& P, const PageWs& W, const int32_t* src,
     }
     return;
   }
-  const int64_t full = n / P.chunk, rest = n % P.chunk;
   const int32_t* from = P.table + (int64_t(src[item]) * P.hkv + g) * P.max_blocks;
   const int32_t page = rest ? __ldcg(W.list + at) : -1;
 #pragma unroll 2
@@ -255,59 +277,62 @@ template <bool kFork>
 __global__ void __launch_bounds__(kBookThreads)
     pages_items_kernel(PoolArgs P, PageWs W, const int32_t* src, const int32_t* dst, const int64_t* tokens, int n_items,
                        bool copy_here) {
+  constexpr int kKeep = 1024;                                // of the list, and of this CTA's rows' offsets
   __shared__ int s_red[kBookWarps];
   __shared__ int64_t s_red64[kBookWarps];
+  __shared__ int32_t s_list[kKeep], s_offs[kKeep];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int id = int(cluster_rank()) * kBookThreads + threadIdx.x, step = int(gridDim.x) * kBookThreads;
-  for (int i = id; i < P.n_seqs; i += step) W.first[i] = INT32_MAX;
-  count_share(P, W, false, s_red);
-  cluster_sync();
-  for (int i = id; i < n_items; i += step) {
-    const int32_t d = dst[i];
-    if (d >= 0 && d < P.n_seqs) atomicMin(W.first + d, i);
-  }
-  const int have = rank_share(P, W, false, s_red, [&](int64_t p, bool c, int rank) {
-    if (c) W.list[rank] = int32_t(p);
-  });
-  cluster_sync();
-  const int64_t rows = int64_t(n_items) * P.hkv;
-  const Share mine = share_of(rows);
-  for (int64_t r = mine.p0 + warp; r < mine.p1; r += kBookWarps) {
-    const int need = row_need<kFork>(P, W, src, dst, tokens, int(r / P.hkv), int(r % P.hkv), lane);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, rows = n_items * P.hkv;
+  const Share pages(int(P.n_pages)), mine(rows);
+  const int32_t* list = n_items <= kKeep ? s_list : dst;
+  int32_t* offs = mine.b - mine.a <= kKeep ? s_offs : W.offs + mine.a;
+  if (n_items <= kKeep && threadIdx.x < n_items) s_list[threadIdx.x] = dst[threadIdx.x];
+  uint32_t bits;
+  const int n = count_share(P, pages, false, &bits);
+  __syncthreads();
+  for (int r = mine.a + warp; r < mine.b; r += kBookWarps) {
+    const int item = r / P.hkv, need = row_need<kFork>(P, src, list, tokens, n_items, item, r - item * P.hkv, lane);
     if (lane == 0) {
       W.need[r] = need;
       if (kFork) W.copy[r] = -1;
     }
   }
+  int sum;
+  block_prefix(n, s_red, &sum);
+  if (threadIdx.x == 0) W.seg[cluster_rank()] = sum;
   cluster_sync();
+  const int2 have = counts_of(W);
+  rank_share(P, pages, false, bits, have.y, s_red, [&](int p, bool c, int rank) {
+    if (c) W.list[rank] = p;
+  });
   // Every CTA ranks all needs and keeps its rows' offsets; a refused head refuses its
   // item (offset -1). Sums may pass 31 bits where no pool could serve them: they are
   // kept in 64, and an offset that does not fit belongs to a call that changes nothing.
   int64_t carry = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kBookThreads) {
-    const int64_t r = r0 + threadIdx.x;
-    int64_t v = 0, sum;
+  for (int r0 = 0; r0 < rows; r0 += kBookThreads) {
+    const int r = r0 + threadIdx.x;
+    int64_t v = 0, all;
     bool ok = false;
     if (r < rows) {
       ok = true;
-      const int64_t i0 = r / P.hkv * P.hkv;
+      const int i0 = r / P.hkv * P.hkv;
+#pragma unroll 4
       for (int g = 0; g < P.hkv; ++g) ok &= __ldcg(W.need + i0 + g) >= 0;
       v = ok ? __ldcg(W.need + r) : 0;
     }
-    const int64_t at = carry + block_prefix(v, s_red64, &sum);
-    if (r >= mine.p0 && r < mine.p1) W.offs[r] = ok ? int32_t(min64(at, INT32_MAX)) : -1;
-    carry += sum;
+    const int64_t at = carry + block_prefix(v, s_red64, &all);
+    if (r >= mine.a && r < mine.b) offs[r - mine.a] = ok ? int32_t(min64(at, INT32_MAX)) : -1;
+    carry += all;
   }
-  if (carry > have) {
-    if (id == 0) flag(P, ZHA_DEV_NO_PAGES);
+  cluster_sync();
+  if (carry > have.x) {
+    if (cluster_rank() == 0 && threadIdx.x == 0) flag(P, ZHA_DEV_NO_PAGES);
     return;
   }
-  __syncthreads();
-  for (int64_t r = mine.p0 + warp; r < mine.p1; r += kBookWarps) {
-    const int at = W.offs[r];
-    if (at >= 0) fill_row<kFork>(P, W, src, dst, tokens, r, at, copy_here, lane);
+  for (int r = mine.a + warp; r < mine.b; r += kBookWarps) {
+    const int at = offs[r - mine.a], item = r / P.hkv;
+    if (at >= 0) fill_row<kFork>(P, W, src, list[item], tokens[item], item, r - item * P.hkv, r, at, copy_here, lane);
   }
 }
 
@@ -387,11 +412,15 @@ __global__ void __launch_bounds__(kBookThreads)
   __shared__ int s_red[kBookWarps];
   pdl_trigger();
   pdl_wait();
-  count_share(P, W, true, s_red);
+  const Share pages(int(P.n_pages));
+  uint32_t bits;
+  int sum;
+  block_prefix(count_share(P, pages, true, &bits), s_red, &sum);
+  if (threadIdx.x == 0) W.seg[cluster_rank()] = sum;
   cluster_sync();
-  int n = 0;
-  for (int i = 0; i < int(gridDim.x); ++i) n += __ldcg(W.seg + i);
-  rank_share(P, W, true, s_red, [&](int64_t p, bool live, int rank) {
+  const int2 counts = counts_of(W);
+  const int n = counts.x;
+  rank_share(P, pages, true, bits, counts.y, s_red, [&](int p, bool live, int rank) {
     int32_t code = -1;
     if (live) {
       code = int32_t(p);
@@ -513,7 +542,7 @@ template <bool kFork>
 zha_status run_items(const PoolArgs& P, const int32_t* src, const int32_t* dst, const int64_t* tokens, int32_t n_items,
                      void* d_ws, size_t ws_bytes, cudaStream_t s, const char* who) {
   const int64_t rows = int64_t(n_items) * P.hkv;
-  const PageWs W = page_ws(d_ws, P.n_pages, P.n_seqs, rows);
+  const PageWs W = page_ws(d_ws, P.n_pages, rows);
   zha_status st = need_ws(d_ws, ws_bytes, W.bytes);
   if (st != ZHA_OK) return st;
   const bool copy_here = rows * P.chunk * P.row_bytes <= kCopyHere;
@@ -536,7 +565,7 @@ size_t zha_pages_workspace_bytes(const zha_config* cfg, const zha_page_pool* poo
   if (zha::pool_args(cfg, pool, "zha_pages_workspace_bytes", &P) != ZHA_OK || n_items < 0 || n_items > 65535 ||
       int64_t(n_items) * P.hkv > zha::kMaxItemRows)
     return 0;
-  return size_t(zha::page_ws(nullptr, P.n_pages, P.n_seqs, int64_t(n_items) * P.hkv).bytes);
+  return size_t(zha::page_ws(nullptr, P.n_pages, int64_t(n_items) * P.hkv).bytes);
 }
 
 zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_seqs,
@@ -585,7 +614,7 @@ zha_status zha_pages_compact(const zha_config* cfg, const zha_page_pool* pool, i
   zha_status st = zha::pool_args(cfg, pool, who, &P);
   if (st != ZHA_OK) return st;
   P.status = d_status;
-  const zha::PageWs W = zha::page_ws(d_ws, P.n_pages, P.n_seqs, 0);
+  const zha::PageWs W = zha::page_ws(d_ws, P.n_pages, 0);
   if ((st = zha::need_ws(d_ws, ws_bytes, W.bytes)) != ZHA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
