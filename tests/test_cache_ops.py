@@ -135,6 +135,43 @@ def test_attend_splits_long_sequences(zha, cache, q, G, n):
     b.check(*b.run())
 
 
+@pytest.mark.parametrize("cache,q,H,G,d,C,lens", [
+    (BF, F32, 2, 4, 64, 16, [(i * 1009) % 24000 for i in range(45)]),
+    (BF, BF, 1, 9, 128, 64, [230000, 0, 3, 180001, 60000]),
+    (F32, F32, 2, 3, 128, 7, [(i * 611) % 7000 + 1 for i in range(40)])])
+def test_attend_long_batches_dealt_in_two_parts(zha, cache, q, H, G, d, C, lens):
+    """More keys than the first deal gives out: units end in either part and across both."""
+    b = Batch(zha, lens, H, G, d, C, cache, q, seed=14)
+    out, lse = b.run()
+    b.check(out, lse)
+    out2, lse2 = b.run()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_attend_few_tokens_in_a_call_made_for_many(zha):
+    """The launch is sized by max_tokens; the counts in device memory may be anything below,
+    also in a replayed graph."""
+    b = Batch(zha, [3, 0, 70], 2, 4, 64, 16, BF, F32, paged=False, seed=15)
+    ld = 200000
+    K, V = (torch.zeros(3, 2, ld, 64, dtype=BF, device="cuda") for _ in range(2))
+    K[:, :, :70], V[:, :, :70] = b.K[:, :, :70].nan_to_num(), b.V[:, :, :70].nan_to_num()
+    g = _gen(16)
+    K[1, :, 1000:ld] = torch.randn(2, ld - 1000, 64, device="cuda", generator=g).to(BF)
+    V[1, :, 1000:ld] = torch.randn(2, ld - 1000, 64, device="cuda", generator=g).to(BF)
+    b.K, b.V, b.most = K, V, ld
+    b.kv = zha.kv_batch(K, V)
+    b.check(*b.run())
+    out, lse = torch.empty_like(b.Q), torch.empty(3, 8, device="cuda")
+    ws = torch.empty(zha.attend_batch_workspace_bytes(b.cfg, 3, ld), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run(out=out, lse=lse, ws=ws)
+    for lens in ([0, 0, 1], [3, ld, 70], [0, 0, 0], [70, 131072, 33]):
+        b.n.copy_(torch.tensor(lens))
+        graph.replay()
+        b.check(out, lse)
+
+
 def test_attend_many_short_sequences(zha):
     lens = [(i * 37) % 200 for i in range(700)]
     b = Batch(zha, lens, 2, 2, 64, 16, BF, F32, seed=4)
@@ -320,6 +357,18 @@ def test_rope_apply_matches_the_formula_and_its_inverse(zha, src, dst, layout, d
             _close(out, *_turn64(x, pos, args, back))
 
 
+@pytest.mark.parametrize("layout,pairs,d,dt", [("half", 64, 128, BF), ("interleaved", 24, 64, F32), ("half", 11, 64, BF)])
+@pytest.mark.parametrize("T,H", [(3, 200), (700, 40), (3000, 2), (601, 17), (4099, 1)])
+def test_rope_apply_over_shapes_of_work(zha, layout, pairs, d, dt, T, H):
+    """Few tokens with many rows, many with few, and sizes that end inside a block."""
+    args = dict(pairs=pairs, layout=layout)
+    g = _gen(25)
+    x = torch.randn(T, H, d, device="cuda", generator=g).to(dt)
+    pos = torch.randint(0, 100000, (T,), device="cuda", generator=g)
+    want, tol = _turn64(x, pos, args)
+    _close(zha.rope_apply(zha.Rope(d, **args), x, pos, out=x), want, tol)
+
+
 def test_rope_far_positions(zha):
     """A million, 2^31 and 2^40 tokens on, where an fp32 product of position and
     frequency has lost the angle. The table holds theta / 2 pi < 2^-2 to 2^-54: powers of
@@ -452,6 +501,17 @@ def test_append_writes_turned_keys_values_and_queries(zha, src, cache, q, layout
     out = _append_run(c, pos, status=st)
     assert out.dtype == q and int(st) == 0
     _append_check(c, out, pos)
+
+
+@pytest.mark.parametrize("d,H,G,C,T,S", [(128, 1, 3, 16, 2500, 7), (64, 3, 5, 64, 1300, 2), (128, 8, 8, 5, 2, 2)])
+def test_append_over_shapes_of_work(zha, d, H, G, C, T, S):
+    c = _append_case(zha, BF, BF, F32, "half", d // 4, d, H, G, C, T, S, True, seed=36)
+    c["seq"][T // 2] = -1
+    pos = c["index"] + 5
+    q_out = torch.full((T, H * G, d), 5.0, device="cuda")
+    out = _append_run(c, pos, q_out=q_out)
+    assert (out[T // 2] == 5).all()
+    _append_check(c, out, pos, drop={T // 2})
 
 
 def test_append_without_rotation_queries_or_positions(zha):
@@ -710,6 +770,26 @@ def test_pages_all_or_nothing_refusals_and_edges(zha):
     assert p.fork([3], [2], [4]) == z.ZHA_DEV_BAD_PAGE
     assert p.compact() == z.ZHA_DEV_BAD_PAGE and p.t[3, 0].tolist() == [-1, 0, 1 << 30, -1]
     assert p.free([3]) == z.ZHA_DEV_BAD_PAGE
+
+
+def test_pages_long_lists(zha):
+    """More items than a CTA keeps of a list, and more rows than it keeps offsets of."""
+    rng = np.random.default_rng(7)
+    S, H = 5000, 4
+    p = Pages(zha, S, H, 2, 3, 60000)
+    order = [int(x) for x in rng.permutation(S)]
+    assert p.extend(order, [int(x) for x in rng.integers(0, 7, S)]) == 0
+    half = order[:2500]
+    assert p.free(half) == 0
+    n = _lens(p)
+    src = [order[2500 + i] for i in range(2500)]
+    tok = [int(rng.integers(0, 2 * n[s] + 1)) for s in src]
+    assert p.fork(src, half, tok) == 0
+    # the same sequence far apart in one list: the later item is refused
+    twice = order[:3000] + [order[5]]
+    assert p.extend(twice, [6] * 3000 + [2]) == zha.ZHA_DEV_BAD_SEQUENCE
+    p.compact()
+    assert p.extend(order, [6] * S) in (0, zha.ZHA_DEV_NO_PAGES)
 
 
 def test_pages_captured_with_one_workspace(zha):
