@@ -386,7 +386,10 @@ struct Queries {
   }
 };
 
-// o[q][tile of 16 elements] += V^T * weights; p as the scores.
+// o[q][tile of 16 elements] += V^T * weights; p as the scores. The matrix instructions
+// cut their sums off instead of rounding them, which over a long cache adds up (1M
+// keys: 9e-6 of the largest output): they sum a tile's keys alone, from zero, and o is
+// summed by rounded additions (1e-6).
 template <typename Kv, int D, int HU, int TERMS, int NB>
 __device__ __forceinline__ void add_values(uint32_t tile_at, const char* tile, int lane,
                                            float (&p)[Columns<HU>::kTiles][NB][2],
@@ -425,12 +428,17 @@ __device__ __forceinline__ void add_values(uint32_t tile_at, const char* tile, i
                        : "r"(tile_at + Tile<Kv, D>::at_v(row, 2 * (d0 + i) + ((lane >> 3) & 1)))
                        : "memory");
 #pragma unroll
-        for (int k = kOps - 1; k >= 0; --k)
+        for (int q = 0; q < kTiles; ++q) {
+          float c[4][4] = {};
 #pragma unroll
-          for (int q = 0; q < kTiles; ++q)
+          for (int k = kOps - 1; k >= 0; --k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16(o[q][d0 + i], v[i][0], v[i][1], v[i][2], v[i][3], w[q][k][0], w[q][k][1]);
+            for (int i = 0; i < 4; ++i) mma_bf16(c[i], v[i][0], v[i][1], v[i][2], v[i][3], w[q][k][0], w[q][k][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[q][d0 + i][j] += c[i][j];
+        }
       }
     }
   } else {
@@ -467,14 +475,17 @@ __device__ __forceinline__ void add_values(uint32_t tile_at, const char* tile, i
           for (int r = 0; r < 4; ++r) split_tf32(v[i][r], one[i][r], two[i][r]);
 #pragma unroll
         for (int q = 0; q < kTiles; ++q) {
+          float e[4][4] = {};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_tf32(o[q][4 * j + i], two[i][0], two[i][1], two[i][2], two[i][3], w[q][0][0], w[q][0][1]);
+          for (int i = 0; i < 4; ++i) mma_tf32(e[i], two[i][0], two[i][1], two[i][2], two[i][3], w[q][0][0], w[q][0][1]);
 #pragma unroll
           for (int k = kOps - 1; k >= 0; --k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_tf32(o[q][4 * j + i], one[i][0], one[i][1], one[i][2], one[i][3], w[q][k][0], w[q][k][1]);
+            for (int i = 0; i < 4; ++i) mma_tf32(e[i], one[i][0], one[i][1], one[i][2], one[i][3], w[q][k][0], w[q][k][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[q][4 * j + i][r] += e[i][r];
         }
       }
     }
