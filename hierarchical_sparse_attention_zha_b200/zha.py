@@ -118,7 +118,7 @@ def kv_batch(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor | None 
     c.dtype = _DTYPE[K.dtype]
     c.seqs = K.shape[0] if block_table is None else block_table.shape[0]
     c.heads = K.shape[1] if block_table is None else block_table.shape[1]
-    c.device = K.device
+    c.device, c.index = K.device, K.get_device()
     return c
 
 
@@ -448,34 +448,47 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-# (Each check is an `if` of its own: a small call's time on the host is what it costs.)
+# A small call costs its time on the host, so the checks below are plain comparisons,
+# devices are compared by number, and pointers go to C as integers.
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-def _run_on(device, stream) -> int:
-    """The stream of a call on tensors of `device`, which must be the current one."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+
+def _run_on(index: int, stream) -> int:
+    """The stream of a call on tensors of device `index` (-1: not a GPU), which must be the
+    current one. (torch.cuda.current_stream() makes an object of it, which takes 3 us.)"""
+    if index < 0 or index != _get_device():
         raise ValueError("tensors must lie on the current CUDA device")
-    # (torch.cuda.current_stream() makes an object of it, which takes 3 us)
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
-def _status_ptr(status: torch.Tensor | None, device):
+def _status_ptr(status: torch.Tensor | None, index: int):
     if status is None:
         return None
-    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
+    if status.dtype is not torch.int32 or status.get_device() != index or status.numel() < 1:
         raise ValueError("status must be an int32 tensor on the same device")
     return status.data_ptr()
 
 
-def _scratch(ws: torch.Tensor, device) -> tuple[int, int]:
-    if ws.device != device or not ws.is_contiguous():
+def _scratch(ws: torch.Tensor, index: int) -> tuple[int, int]:
+    if ws.get_device() != index or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the same device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _list_ptr(x: torch.Tensor, dtype, n: int, device, name: str) -> int:
-    if x.dtype != dtype or x.device != device or x.shape != (n,) or not x.is_contiguous():
+def _list_ptr(x: torch.Tensor, dtype, n: int, index: int, name: str) -> int:
+    if x.dtype is not dtype or x.get_device() != index or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] on the same device")
     return x.data_ptr()
+
+
+_three_rows = c_int64 * 9                        # zha_rows one behind the other
+
+
+def _row_args(x: torch.Tensor, shape: tuple, index: int, name: str) -> tuple[int, int, int]:
+    stride = x.stride()
+    if x.shape != shape or x.get_device() != index or stride[2] != 1:
+        raise ValueError(f"{name} must be {list(shape)} with rows of adjacent elements, on the same device")
+    return x.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
 def _same_cache(cfg: Config, c) -> None:
@@ -502,32 +515,31 @@ class Rope:
                         self.SCALINGS[scaling], freq_dim, 0, base, factor, original_tokens, low, high, amplitude)
         self.table = RopeTable()
         check(lib.zha_rope_init(byref(spec), byref(self.table)), "zha_rope_init")
-
-
-def _rows(x: torch.Tensor, shape: tuple, device, name: str) -> Rows:
-    stride = x.stride()
-    if x.shape != shape or x.device != device or (stride[2] != 1 and x.numel() > 0):
-        raise ValueError(f"{name} must be {list(shape)} with rows of adjacent elements, on the same device")
-    return Rows(x.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
+        self.at = ctypes.addressof(self.table)
 
 
 def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | None = None,
                inverse: bool = False, stream=None) -> torch.Tensor:
     """zha_rope_apply: x [T, heads, d] (float32 or bf16, any token and head strides) turned
     at pos [T] int64, or turned back (the gradient's direction). `out` may be x."""
-    shape, dev, dtype = x.shape, x.device, _DTYPE.get(x.dtype)
+    shape, index, dtype = x.shape, x.get_device(), _DTYPE.get(x.dtype)
     if len(shape) != 3 or dtype is None or shape[2] != rope.table.head_dim:
         raise ValueError("x must be [T, heads, head_dim] of the rotation, float32 or bfloat16")
-    on = _run_on(dev, stream)
+    on = _run_on(index, stream)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
     to = _DTYPE.get(out.dtype)
     if to is None:
         raise ValueError("out must be float32 or bfloat16")
-    rx = _rows(x, shape, dev, "x")
-    ry = rx if out is x else _rows(out, shape, dev, "out")
-    check(lib.zha_rope_apply(byref(rope.table), byref(rx), dtype, _list_ptr(pos, torch.int64, shape[0], dev, "pos"),
-                             shape[0], shape[1], 1 if inverse else 0, byref(ry), to, on), "zha_rope_apply")
+    T, H, _ = shape
+    where = _list_ptr(pos, torch.int64, T, index, "pos")
+    if T == 0 or H == 0:
+        return out
+    rows = _three_rows(*_row_args(x, shape, index, "x"), *_row_args(out, shape, index, "out"))
+    at = ctypes.addressof(rows)
+    st = lib.zha_rope_apply(rope.at, at, dtype, where, T, H, inverse, at + 24, to, on)
+    if st:
+        check(st, "zha_rope_apply")
     return out
 
 
@@ -541,29 +553,30 @@ def rope_append_kv(cfg: Config, rope: Rope | None, q: torch.Tensor | None, k: to
     _same_cache(cfg, kv)
     if not 1 <= n_seqs <= kv.seqs:
         raise ValueError("n_seqs is more than the caches hold")
-    H, Hq, d = cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
-    T, dev, dtype = k.shape[0], kv.device, _DTYPE.get(k.dtype)
+    H, Hq, d, dev = cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim, kv.index
+    T, dtype = k.shape[0], _DTYPE.get(k.dtype)
     on = _run_on(dev, stream)
-    if dtype is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    if dtype is None or v.dtype is not k.dtype or (q is not None and q.dtype is not k.dtype):
         raise ValueError("q, k and v must have one type, float32 or bfloat16")
-    shape = (T, H, d)
-    rk, rv = _rows(k, shape, dev, "k"), _rows(v, shape, dev, "v")
-    rq = to = None
-    q_type = ZHA_F32
+    to, q_type, q_rows = None, ZHA_F32, (0, 0, 0)
     if q is not None:
         shape = (T, Hq, d)
-        rq = byref(_rows(q, shape, dev, "q"))
         if q_out is None:
-            q_out = torch.empty(shape, dtype=q_dtype, device=dev)
+            q_out = torch.empty(shape, dtype=q_dtype, device=kv.device)
         q_type = _DTYPE.get(q_out.dtype)
-        if q_type is None or q_out.shape != shape or q_out.device != dev or not q_out.is_contiguous():
+        if q_type is None or q_out.shape != shape or q_out.get_device() != dev or not q_out.is_contiguous():
             raise ValueError(f"q_out must be a contiguous float32 or bfloat16 tensor {list(shape)}")
         to = q_out.data_ptr()
-    check(lib.zha_rope_append_kv(
-        byref(cfg), None if rope is None else byref(rope.table), rq, byref(rk), byref(rv), dtype, T, byref(kv), n_seqs,
-        _list_ptr(seq, torch.int32, T, dev, "seq"), _list_ptr(index, torch.int64, T, dev, "index"),
-        None if pos is None else _list_ptr(pos, torch.int64, T, dev, "pos"), to, q_type, _status_ptr(status, dev), on),
-        "zha_rope_append_kv")
+        q_rows = _row_args(q, shape, dev, "q")
+    shape = (T, H, d)
+    rows = _three_rows(*_row_args(k, shape, dev, "k"), *_row_args(v, shape, dev, "v"), *q_rows)
+    at = ctypes.addressof(rows)
+    st = lib.zha_rope_append_kv(
+        byref(cfg), None if rope is None else rope.at, None if q is None else at + 48, at, at + 24, dtype, T, byref(kv),
+        n_seqs, _list_ptr(seq, torch.int32, T, dev, "seq"), _list_ptr(index, torch.int64, T, dev, "index"),
+        None if pos is None else _list_ptr(pos, torch.int64, T, dev, "pos"), to, q_type, _status_ptr(status, dev), on)
+    if st:
+        check(st, "zha_rope_append_kv")
     return None if q is None else q_out
 
 
@@ -579,25 +592,26 @@ def attend_batch_kv(cfg: Config, Q: torch.Tensor, kv: KvCache, n_seqs: int, n_to
     _same_cache(cfg, kv)
     if not 1 <= n_seqs <= kv.seqs:
         raise ValueError("n_seqs is more than the caches hold")
-    dev, dtype = kv.device, _DTYPE.get(Q.dtype)
+    dev, dtype = kv.index, _DTYPE.get(Q.dtype)
     on = _run_on(dev, stream)
     want = (n_seqs, cfg.n_q_heads, cfg.head_dim)
-    if dtype is None or Q.shape != want or Q.device != dev or not Q.is_contiguous():
+    if dtype is None or Q.shape != want or Q.get_device() != dev or not Q.is_contiguous():
         raise ValueError(f"Q must be a contiguous float32 or bfloat16 tensor {list(want)} on the cache's device")
     if out is None:
         out = torch.empty_like(Q)
-    elif out.shape != want or out.dtype != Q.dtype or out.device != dev or not out.is_contiguous():
+    elif out.shape != want or out.dtype is not Q.dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of Q's shape and type")
     if lse is None:
-        lse = torch.empty(want[:2], dtype=torch.float32, device=dev)
-    elif lse.shape != want[:2] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        lse = torch.empty(want[:2], dtype=torch.float32, device=kv.device)
+    elif lse.shape != want[:2] or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [n_seqs, Hq]")
     if ws is None:
-        ws = _bytes_tensor(attend_batch_workspace_bytes(cfg, n_seqs, max_tokens), dev)
-    check(lib.zha_attend_batch_kv(byref(cfg), Q.data_ptr(), dtype, byref(kv), n_seqs,
-                                  _list_ptr(n_tokens, torch.int64, n_seqs, dev, "n_tokens"), max_tokens, out.data_ptr(),
-                                  lse.data_ptr(), *_scratch(ws, dev), _status_ptr(status, dev), on),
-          "zha_attend_batch_kv")
+        ws = _bytes_tensor(attend_batch_workspace_bytes(cfg, n_seqs, max_tokens), kv.device)
+    st = lib.zha_attend_batch_kv(byref(cfg), Q.data_ptr(), dtype, byref(kv), n_seqs,
+                                 _list_ptr(n_tokens, torch.int64, n_seqs, dev, "n_tokens"), max_tokens, out.data_ptr(),
+                                 lse.data_ptr(), *_scratch(ws, dev), _status_ptr(status, dev), on)
+    if st:
+        check(st, "zha_attend_batch_kv")
     return out, lse
 
 
@@ -607,9 +621,10 @@ def page_pool(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor, refs:
     _need(block_table is not None, "a page pool needs a block table")
     kv = kv_batch(K, V, block_table)
     p = PagePool(kv.k, kv.v, kv.ld, kv.block_table, kv.max_blocks,
-                 _list_ptr(refs, torch.int32, K.shape[0], K.device, "refs"), block_table.shape[0], 0)
+                 _list_ptr(refs, torch.int32, K.shape[0], K.get_device(), "refs"), block_table.shape[0], 0)
     p.tensors = (*kv.tensors, refs)
-    p.shape, p.dtype, p.heads, p.seqs, p.device = kv.shape, kv.dtype, kv.heads, kv.seqs, kv.device
+    p.shape, p.dtype, p.heads, p.seqs, p.device, p.index = (kv.shape, kv.dtype, kv.heads, kv.seqs,
+                                                                   kv.device, kv.index)
     return p
 
 
@@ -621,27 +636,31 @@ def pages_extend(cfg: Config, pool: PagePool, seqs: torch.Tensor, n_tokens: torc
                  ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_extend: pages for the first n_tokens[i] (int64) tokens of sequence seqs[i] (int32)."""
     _same_cache(cfg, pool)
-    n, dev = seqs.numel(), pool.device
+    n, dev = seqs.numel(), pool.index
     on = _run_on(dev, stream)
     if ws is None:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), dev)
-    check(lib.zha_pages_extend(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
-                               _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
-                               _status_ptr(status, dev), on), "zha_pages_extend")
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), pool.device)
+    st = lib.zha_pages_extend(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
+                              _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
+                              _status_ptr(status, dev), on)
+    if st:
+        check(st, "zha_pages_extend")
 
 
 def pages_fork(cfg: Config, pool: PagePool, src: torch.Tensor, dst: torch.Tensor, n_tokens: torch.Tensor,
                ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_fork: the empty sequence dst[i] becomes the first n_tokens[i] tokens of src[i]."""
     _same_cache(cfg, pool)
-    n, dev = dst.numel(), pool.device
+    n, dev = dst.numel(), pool.index
     on = _run_on(dev, stream)
     if ws is None:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), dev)
-    check(lib.zha_pages_fork(byref(cfg), byref(pool), _list_ptr(src, torch.int32, n, dev, "src"),
-                             _list_ptr(dst, torch.int32, n, dev, "dst"),
-                             _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
-                             _status_ptr(status, dev), on), "zha_pages_fork")
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), pool.device)
+    st = lib.zha_pages_fork(byref(cfg), byref(pool), _list_ptr(src, torch.int32, n, dev, "src"),
+                            _list_ptr(dst, torch.int32, n, dev, "dst"),
+                            _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
+                            _status_ptr(status, dev), on)
+    if st:
+        check(st, "zha_pages_fork")
 
 
 def pages_free(cfg: Config, pool: PagePool, seqs: torch.Tensor, keep: torch.Tensor | None = None,
@@ -649,11 +668,13 @@ def pages_free(cfg: Config, pool: PagePool, seqs: torch.Tensor, keep: torch.Tens
     """zha_pages_free: sequences seqs [n] give up their pages behind the first keep [n] (int64)
     tokens (None: all). Needs no workspace; ws is taken for symmetry and not used."""
     _same_cache(cfg, pool)
-    n, dev = seqs.numel(), pool.device
+    n, dev = seqs.numel(), pool.index
     on = _run_on(dev, stream)
-    check(lib.zha_pages_free(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
-                             None if keep is None else _list_ptr(keep, torch.int64, n, dev, "keep"), n,
-                             _status_ptr(status, dev), on), "zha_pages_free")
+    st = lib.zha_pages_free(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
+                            None if keep is None else _list_ptr(keep, torch.int64, n, dev, "keep"), n,
+                            _status_ptr(status, dev), on)
+    if st:
+        check(st, "zha_pages_free")
 
 
 def pages_compact(cfg: Config, pool: PagePool, page_map: torch.Tensor | None = None, n_live: torch.Tensor | None = None,
@@ -661,12 +682,14 @@ def pages_compact(cfg: Config, pool: PagePool, page_map: torch.Tensor | None = N
     """zha_pages_compact: the pages in use become [0, n); page_map [n_pages] and n_live [1]
     (int32, both may be None) say where each went and how many they are."""
     _same_cache(cfg, pool)
-    dev = pool.device
+    dev = pool.index
     on = _run_on(dev, stream)
     if ws is None:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, 0), dev)
-    check(lib.zha_pages_compact(
+        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, 0), pool.device)
+    st = lib.zha_pages_compact(
         byref(cfg), byref(pool),
         None if page_map is None else _list_ptr(page_map, torch.int32, pool.shape[0], dev, "page_map"),
         None if n_live is None else _list_ptr(n_live, torch.int32, 1, dev, "n_live"), *_scratch(ws, dev),
-        _status_ptr(status, dev), on), "zha_pages_compact")
+        _status_ptr(status, dev), on)
+    if st:
+        check(st, "zha_pages_compact")
