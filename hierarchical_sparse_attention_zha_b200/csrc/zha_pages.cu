@@ -172,11 +172,20 @@ __device__ void rank_share(const PoolArgs& P, const Share& h, bool live, uint32_
   }
 }
 
+// (All loads of a round before its stores: the compiler may not move them there.)
 __device__ __forceinline__ void copy_bytes(char* to, const char* from, int64_t n, int id, int step) {
+  constexpr int kRound = 8;
   const uint4* f = reinterpret_cast<const uint4*>(from);
   uint4* t = reinterpret_cast<uint4*>(to);
-#pragma unroll 4
-  for (int64_t i = id; i < n / 16; i += step) t[i] = f[i];
+  for (int64_t i = id; i < n / 16; i += kRound * step) {
+    uint4 x[kRound];
+#pragma unroll
+    for (int j = 0; j < kRound; ++j)
+      if (i + j * step < n / 16) x[j] = f[i + j * step];
+#pragma unroll
+    for (int j = 0; j < kRound; ++j)
+      if (i + j * step < n / 16) t[i + j * step] = x[j];
+  }
 }
 __device__ __forceinline__ void copy_rows(const PoolArgs& P, int32_t to, int32_t from, int64_t rows, int id, int step) {
   const int64_t f = int64_t(from) * P.chunk * P.row_bytes, t = int64_t(to) * P.chunk * P.row_bytes;
@@ -384,16 +393,27 @@ __global__ void __launch_bounds__(kPageThreads)
 __device__ void move_pages(const PoolArgs& P, const PageWs& W, int32_t* page_map, int32_t* n_live) {
   const int moves = __ldcg(W.scal + kMoves), threads = blockDim.x;
   auto place = [&](int32_t code) { return code < -1 ? __ldcg(W.list + moves - 1 - (-2 - code)) : code; };
-  for (int k = blockIdx.x; k < moves; k += gridDim.x) {
-    const int32_t to = __ldcg(W.list + k), from = __ldcg(W.list + P.n_pages - 1 - (moves - 1 - k));
-    copy_rows(P, to, from, P.chunk, threadIdx.x, threads);
-    if (threadIdx.x == 0) {
-      P.refs[to] = P.refs[from];
-      P.refs[from] = 0;
-    }
+  auto from_of = [&](int64_t k) { return __ldcg(W.list + P.n_pages - 1 - (moves - 1 - k)); };
+  // 4 KB of K or V a warp and step, so that few large pages fill the GPU evenly
+  // (a page a block: 7 rounds for the work of 6.2 at 7,300 pages).
+  constexpr int kPart = 4096;
+  const int64_t page_bytes = int64_t(P.chunk) * P.row_bytes;
+  const int half = int((page_bytes + kPart - 1) / kPart), parts = 2 * half, lane = threadIdx.x % 32;
+  const int64_t warps = int64_t(gridDim.x) * (threads / 32);
+  for (int64_t u = int64_t(blockIdx.x) * (threads / 32) + threadIdx.x / 32; u < int64_t(moves) * parts; u += warps) {
+    const int64_t k = quotient(u, parts);
+    const int part = int(u - k * parts), at = part % half * kPart;
+    const int64_t to = __ldcg(W.list + k) * page_bytes + at, from = from_of(k) * page_bytes + at;
+    char* pool = part < half ? P.k : P.v;
+    copy_bytes(pool + to, pool + from, min64(kPart, page_bytes - at), lane, 32);
   }
   const int64_t cells = int64_t(P.n_seqs) * P.hkv * P.max_blocks, step = int64_t(gridDim.x) * threads;
   const int64_t id = int64_t(blockIdx.x) * threads + threadIdx.x;
+  for (int64_t k = id; k < moves; k += step) {
+    const int32_t to = __ldcg(W.list + k), from = from_of(k);
+    P.refs[to] = P.refs[from];
+    P.refs[from] = 0;
+  }
 #pragma unroll 4
   for (int64_t i = id; i < cells; i += step) {
     const int32_t e = P.table[i];
