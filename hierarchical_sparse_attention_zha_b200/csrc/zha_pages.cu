@@ -75,7 +75,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // All of the cluster's threads, with what they wrote to global memory. What another
 // CTA wrote is then read past L1 (__ldcg).
 __device__ __forceinline__ void cluster_sync() {
-  __threadfence();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -109,38 +108,40 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int32_t b) {
   return (a >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
-// This CTA's share of n things (n < 2^30), in fours.
+// This CTA's share of n things (n < 2^30), in eights.
 struct Share {
   int a, b;
   __device__ explicit Share(int n) {
-    const int per = (n + int(gridDim.x) * 4 - 1) / (int(gridDim.x) * 4) * 4;
+    const int per = (n + int(gridDim.x) * 8 - 1) / (int(gridDim.x) * 8) * 8;
     a = min(n, int(cluster_rank()) * per);
     b = min(n, a + per);
   }
 };
 
-// Which of the pages p..p + 3 below `end` count, as bits.
+// Which of the pages p..p + 7 below `end` count, as bits.
 __device__ __forceinline__ uint32_t counted_bits(const int32_t* refs, int p, int end, bool live) {
   uint32_t bits = 0;
-  if (p + 4 <= end && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
-    const int4 r = *reinterpret_cast<const int4*>(refs + p);
-    bits = uint32_t(counted(r.x, live)) | uint32_t(counted(r.y, live)) << 1 | uint32_t(counted(r.z, live)) << 2 |
-           uint32_t(counted(r.w, live)) << 3;
+  if (p + 8 <= end && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+    const int4 r[2] = {*reinterpret_cast<const int4*>(refs + p), *reinterpret_cast<const int4*>(refs + p + 4)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      bits |= (uint32_t(counted(r[i].x, live)) | uint32_t(counted(r[i].y, live)) << 1 |
+               uint32_t(counted(r[i].z, live)) << 2 | uint32_t(counted(r[i].w, live)) << 3) << (4 * i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
       if (p + i < end && counted(refs[p + i], live)) bits |= 1u << i;
   }
   return bits;
 }
 
 // Pass 1: this thread's part of the share's count. `bits` keeps the share's first
-// 4096 pages' for pass 2.
+// 8192 pages' for pass 2.
 __device__ int count_share(const PoolArgs& P, const Share& h, bool live, uint32_t* bits) {
-  *bits = counted_bits(P.refs, h.a + int(threadIdx.x) * 4, h.b, live);
+  *bits = counted_bits(P.refs, h.a + int(threadIdx.x) * 8, h.b, live);
   int n = __popc(*bits);
 #pragma unroll 4
-  for (int p = h.a + (int(threadIdx.x) + kBookThreads) * 4; p < h.b; p += kBookThreads * 4)
+  for (int p = h.a + (int(threadIdx.x) + kBookThreads) * 8; p < h.b; p += kBookThreads * 8)
     n += __popc(counted_bits(P.refs, p, h.b, live));
   return n;
 }
@@ -156,13 +157,13 @@ __device__ int2 counts_of(const PageWs& W) {
 // Pass 2: f(page, counted, exclusive rank) for the share's pages.
 template <typename F>
 __device__ void rank_share(const PoolArgs& P, const Share& h, bool live, uint32_t bits, int base, int* s_red, F f) {
-  for (int q = h.a; q < h.b; q += kBookThreads * 4) {
-    const int p = q + int(threadIdx.x) * 4;
+  for (int q = h.a; q < h.b; q += kBookThreads * 8) {
+    const int p = q + int(threadIdx.x) * 8;
     if (q > h.a) bits = counted_bits(P.refs, p, h.b, live);
     int sum;
     int rank = base + block_prefix(int(__popc(bits)), s_red, &sum);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       if (p + i >= h.b) break;
       const bool c = (bits >> i) & 1u;
       f(p + i, c, rank);
