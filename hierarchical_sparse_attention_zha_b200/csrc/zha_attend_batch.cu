@@ -35,6 +35,13 @@
 //   fp32 cache: every operand is two tf32 terms (cut, then rounded: 2^-22), and of
 //   weight times value the product of the two second terms (2^-11 of the weight, 2^-10
 //   of the value) is left out where it would take an instruction of its own.
+// Measured (held for half a second; the copy rate is 6.55 TB/s): 1M bf16 tokens of 4 KV
+// heads with 8 fp32 query heads each in 338 us (6.35 TB/s, 97%); 8 sequences up to 32K
+// of 8 KV heads, 4 bf16 query heads each, in 103 us (5.85 TB/s, 89%); 160 ragged ones up
+// to 3001 in 94 us (77%). A call starts to read after 3 us, the slowest SMs are done
+// 8 us after the mean, and the join takes 4 us, whatever the length. One
+// bulk copy per row instead of 16 cp.async of 16 bytes: 495 us for the 1M tokens, 17
+// cycles of an SM each.
 #include <cmath>
 
 #include "zha_host.cuh"
@@ -51,12 +58,23 @@ constexpr int kTileBytes = 4096;        // of K, and of V
 constexpr int kMaxSms = 148;
 constexpr int kMaxCtas = kMaxSms * 4;   // two a SM at a time, twice
 constexpr int kMaxWarps = kMaxCtas * kWarps;
-constexpr int kTwoTiers = 24;           // tiles a warp from which the second deal pays
+// The second deal pays from some tiles a warp on (8 x 32K tokens, 4 heads a unit: 102.5
+// us with it, 106.5 without; 160 ragged sequences 92.9, 94.9), but not where the
+// products, not the reads, take the time (12 heads: 142.9 with it, 135.3 without).
+constexpr int kTwoTiers = 24;
 constexpr int kMinTiles = 2;            // no warp takes less, unless there is less
+// Up to so many tiles a unit, and no more units than CTAs at a time, a CTA takes a
+// whole unit and no second kernel is needed (64 sequences of 500 tokens and 4 heads:
+// 12.1 us, split 16.9; 4 of 256 8.5, 11.2; but 4 of 1000 19.0, split 13.1).
 constexpr int kSingleTiles = 32;
 constexpr int kJoinThreads = 256;
-constexpr int kWideUnits = 148;        // up to so many units a CTA joins one head
+// Up to so many units, each in many pieces, a CTA joins one head, else one unit (60K
+// tokens in 4 units: 31.1 us, 36.9 by units).
+constexpr int kWideUnits = 148;
 
+// Heads a unit: the fewest columns that take the group (8 x 32K tokens of 4 heads: 102.5
+// us with 4 columns and two terms side by side, 104.4 with 8; of 12 heads 142.9 with
+// 16, 184.0 with two units of 8, which read the cache twice).
 inline int head_cols(int group) { return group > 8 ? 16 : group > 4 ? 8 : 4; }
 
 struct BatchLayout {
@@ -954,7 +972,7 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   sms = sms < kMaxSms ? sms : kMaxSms;
   const int64_t most = units * tiles;
   A.first_ctas = int32_t(max64(1, min64(sms * 2, (most + kWarps * kMinTiles - 1) / (kWarps * kMinTiles))));
-  A.ctas = most >= int64_t(kTwoTiers) * kWarps * sms * 2 ? sms * 4 : A.first_ctas;
+  A.ctas = HU < 16 && most >= int64_t(kTwoTiers) * kWarps * sms * 2 ? sms * 4 : A.first_ctas;
   const int64_t ctas = A.single ? units : A.ctas;
   {
     TraceScope ts("attend_batch_kernel", 0, s);

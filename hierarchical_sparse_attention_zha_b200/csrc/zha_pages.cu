@@ -12,7 +12,12 @@
 //   3  entries and counts, with every rank known
 // What moves page contents is wide: a second launch over the whole GPU, unless it is
 // small enough to be done by the cluster.
-// Bound: the launch and the passes' latencies; the copied rows (HBM) for compact.
+// Bound: the launch and the passes' latencies (about 12 dependent accesses of 0.6 us);
+// the copied rows (HBM) for compact. Measured: free, fork and extend of a beam of 4 in
+// 18 us on the device together; 48 forks of 128 sequences in 8 x 8300 pages, and all
+// of them extended, in 34 us; 7,300 pages of 32 KB moved in 79 us (6.1 TB/s of reads and
+// writes). As three launches over the whole GPU each, extend and fork took the same
+// time on the device and 9 us more on the host.
 #include <cstdio>
 
 #include "zha_host.cuh"
@@ -26,7 +31,7 @@ constexpr int kPageThreads = 256;         // of the kernels over the whole GPU
 constexpr int kBookThreads = 1024;        // of the cluster's CTAs
 constexpr int kBookWarps = kBookThreads / 32;
 constexpr int kMostCtas = 16;
-constexpr int64_t kCopyHere = 256 << 10;  // bytes the cluster copies itself
+constexpr int64_t kCopyHere = 256 << 10;  // bytes the cluster copies itself (a beam of 4: 20.0 us, 20.5 and a launch without)
 
 struct PoolArgs {
   char* k;
