@@ -9,8 +9,8 @@
 // into tiles of 4 KB of K and 4 KB of V. All units' tiles, one behind the other, are
 // dealt out evenly to the warps from the counts in device memory, so that ragged
 // lengths cost nothing. SMs do not read equally fast (240K tokens: their shares took 58
-// to 78 us), so a long call deals 7/8 of the tiles to the CTAs that the GPU holds at
-// a time, and the rest to as many more, which the SMs that are done first take. A warp keeps its own
+// to 78 us), so a long call deals 11/12 of the tiles to the CTAs that the GPU holds at
+// a time, and the rest to half as many more, which the SMs that are done first take. A warp keeps its own
 // ring of tiles in flight (cp.async), across the borders of units, and waits for no
 // other until its tiles are done. What then becomes of a unit's state:
 //   - all of its tiles in one warp: the warp writes the result;
@@ -36,10 +36,10 @@
 //   weight times value the product of the two second terms (2^-11 of the weight, 2^-10
 //   of the value) is left out where it would take an instruction of its own.
 // Measured (held for half a second; the copy rate is 6.55 TB/s): 1M bf16 tokens of 4 KV
-// heads with 8 fp32 query heads each in 338 us (6.35 TB/s, 97%); 8 sequences up to 32K
-// of 8 KV heads, 4 bf16 query heads each, in 103 us (5.85 TB/s, 89%); 160 ragged ones up
-// to 3001 in 94 us (77%). A call starts to read after 3 us, the slowest SMs are done
-// 8 us after the mean, and the join takes 4 us, whatever the length. One
+// heads with 8 fp32 query heads each in 327 us (6.57 TB/s); 8 sequences up to 32K of 8
+// KV heads, 4 bf16 query heads each, in 98 us (6.15 TB/s, 94%); 160 ragged ones up to 3001
+// in 92 us (79%). A call starts to read after 3 us, the slowest SMs are done
+// some us after the mean, and the join takes 4 us, whatever the length. One
 // bulk copy per row instead of 16 cp.async of 16 bytes: 495 us for the 1M tokens, 17
 // cycles of an SM each.
 #include <cmath>
@@ -56,11 +56,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;              // tiles in a warp's ring
 constexpr int kTileBytes = 4096;        // of K, and of V
 constexpr int kMaxSms = 148;
-constexpr int kMaxCtas = kMaxSms * 4;   // two a SM at a time, twice
+constexpr int kMaxCtas = kMaxSms * 3;   // two a SM at a time, and half as many later
 constexpr int kMaxWarps = kMaxCtas * kWarps;
-// The second deal pays from some tiles a warp on (8 x 32K tokens, 4 heads a unit: 102.5
-// us with it, 106.5 without; 160 ragged sequences 92.9, 94.9), but not where the
-// products, not the reads, take the time (12 heads: 142.9 with it, 135.3 without).
+// The second deal pays from some tiles a warp on (8 x 32K tokens, 4 heads a unit: 100
+// us with it, 106 without; 160 ragged sequences 92, 95), but not where the products, not
+// the reads, take the time (12 heads: 143 with it, 135 without). An eighth to as many
+// CTAs as in the first: 105 and 95; a sixteenth to half as many 102 and 93.
 constexpr int kTwoTiers = 24;
 constexpr int kMinTiles = 2;            // no warp takes less, unless there is less
 // Up to so many tiles a unit, and no more units than CTAs at a time, a CTA takes a
@@ -232,7 +233,7 @@ struct Deal {
   int64_t total, n1, w1, w2;
   Even one, two;
   __device__ static int64_t first_tiles(const BatchArgs& A, int64_t n) {
-    return A.ctas > A.first_ctas && n >= int64_t(kTwoTiers) * kWarps * A.first_ctas ? n - n / 8 : n;
+    return A.ctas > A.first_ctas && n >= int64_t(kTwoTiers) * kWarps * A.first_ctas ? n - n / 12 : n;
   }
   __device__ static int64_t first_warps(const BatchArgs& A, int64_t n) {
     return max64(1, min64(int64_t(A.first_ctas) * kWarps, (n + kMinTiles - 1) / kMinTiles));
@@ -972,7 +973,7 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   sms = sms < kMaxSms ? sms : kMaxSms;
   const int64_t most = units * tiles;
   A.first_ctas = int32_t(max64(1, min64(sms * 2, (most + kWarps * kMinTiles - 1) / (kWarps * kMinTiles))));
-  A.ctas = HU < 16 && most >= int64_t(kTwoTiers) * kWarps * sms * 2 ? sms * 4 : A.first_ctas;
+  A.ctas = HU < 16 && most >= int64_t(kTwoTiers) * kWarps * sms * 2 ? sms * 3 : A.first_ctas;
   const int64_t ctas = A.single ? units : A.ctas;
   {
     TraceScope ts("attend_batch_kernel", 0, s);

@@ -493,7 +493,9 @@ def _row_args(x: torch.Tensor, shape: tuple, index: int, name: str) -> tuple[int
 
 def _same_cache(cfg: Config, c) -> None:
     """A configuration and a kv_batch() or page_pool() that describe one cache."""
-    s = c.shape
+    s = getattr(c, "shape", None)
+    if s is None:
+        raise ValueError("the cache must come from kv_batch() or page_pool()")
     if (c.heads != cfg.n_kv_heads or s[-1] != cfg.head_dim or c.dtype != cfg.kv_dtype
             or (len(s) == 3 and s[1] != cfg.chunk)):
         raise ValueError("the cache does not match the configuration")

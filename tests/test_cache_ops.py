@@ -306,6 +306,35 @@ def test_attend_captured_replayed_with_other_counts_and_streams(zha):
     b.check(out, lse)
 
 
+def test_attend_two_calls_at_once(zha):
+    """Two streams, a workspace each, over one cache."""
+    b = Batch(zha, [40000, 7, 20000], 2, 4, 64, 16, BF, F32, seed=17)
+    want, wlse = b.run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.full_like(b.Q, 9.0), torch.full_like(wlse, 9.0)] for _ in streams]
+    wss = [torch.empty(zha.attend_batch_workspace_bytes(b.cfg, 3, b.most), dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o, w in zip(streams, outs, wss):
+            b.run(out=o[0], lse=o[1], ws=w, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[0], want) and torch.equal(o[1], wlse)
+
+
+def test_batch_calls_refuse_another_calls_cache(zha):
+    b = Batch(zha, [10], 1, 4, 64, 16, BF, F32, seed=18)
+    tree_cache = zha.kv_cache(b.K, b.V, b.table[0].contiguous())       # one sequence's, without what is checked here
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q, tree_cache, 1, b.n, 10)
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q, b.kv, 1, b.n, 10, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q, b.kv, 1, b.n, 10, status=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        zha.attend_batch_kv(b.cfg, b.Q.cpu(), b.kv, 1, b.n, 10)
+
+
 # ---------------------------------------------------------------------------
 # Rotary positions
 # ---------------------------------------------------------------------------
@@ -826,6 +855,41 @@ def test_pages_captured_with_one_workspace(zha):
         zha.pages_extend(p.cfg, p.pool, every, new[:2])
     with pytest.raises(zha.ZhaError):
         zha.pages_extend(p.cfg, p.pool, every, new, ws=ws[:64])
+
+
+def test_append_and_pages_at_the_end_of_a_large_pool(zha):
+    """Rows beyond 2^32 bytes and 2^31 elements: 300,000 pages of 64 rows of 128 bf16."""
+    pages, C, d = 300000, 64, 128
+    K = torch.zeros(pages, C, d, dtype=BF, device="cuda")
+    V = torch.zeros_like(K)
+    table = torch.full((3, 1, 4), -1, dtype=torch.int32, device="cuda")
+    table[0, 0, :2] = torch.tensor([pages - 1, pages - 3], dtype=torch.int32)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[[pages - 1, pages - 3]] = 1
+    refs[: pages - 4] = 5                         # the lowest free pages lie at the end too
+    cfg = _cfg(zha, 1, 2, d, C, BF)
+    pool, kv = zha.page_pool(K, V, table, refs), zha.kv_batch(K, V, table)
+    rope = zha.Rope(d, layout="half")
+    x = torch.randn(100, 4, d, device="cuda", generator=_gen(50)).to(BF)
+    at = torch.arange(100, device="cuda")
+    seq = torch.zeros(100, dtype=torch.int32, device="cuda")
+    st = _status()
+    zha.rope_append_kv(cfg, rope, None, x[:, 2:3], x[:, 3:4], kv, 3, seq, at, status=st)
+    want, tol = _turn64(x[:, 2:3], at, dict(layout="half"))
+    rows = lambda pool, s: pool[table[s, 0].long()[at // C], at % C]
+    _close(rows(K, 0), want[:, 0], tol[:, 0])
+    assert torch.equal(rows(V, 0), x[:, 3])
+    one = lambda v, dt: torch.tensor([v], dtype=dt, device="cuda")
+    zha.pages_fork(cfg, pool, one(0, torch.int32), one(2, torch.int32), one(100, torch.int64), status=st)
+    assert table[2, 0].tolist() == [pages - 1, pages - 4, -1, -1]
+    assert torch.equal(rows(K, 2), rows(K, 0)) and torch.equal(rows(V, 2), rows(V, 0))
+    refs[: pages - 4] = 0
+    before = rows(K, 2).clone(), rows(V, 2).clone()
+    live = _status()
+    zha.pages_compact(cfg, pool, n_live=live, status=st)
+    assert int(live) == 3 and int(st) == 0
+    assert table[:, 0].tolist() == [[2, 1, -1, -1], [-1] * 4, [2, 0, -1, -1]] and refs[:4].tolist() == [1, 1, 2, 0]
+    assert torch.equal(rows(K, 2), before[0]) and torch.equal(rows(V, 2), before[1])
 
 
 # ---------------------------------------------------------------------------
