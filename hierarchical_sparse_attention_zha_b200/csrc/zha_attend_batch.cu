@@ -10,9 +10,9 @@
 // dealt out evenly to the warps from the counts in device memory, so that ragged
 // lengths cost nothing. SMs do not read equally fast (240K tokens: their shares took 58
 // to 78 us), so a long call deals 11/12 of the tiles to the CTAs that the GPU holds at
-// a time, and the rest to half as many more, which the SMs that are done first take. A warp keeps its own
-// ring of tiles in flight (cp.async), across the borders of units, and waits for no
-// other until its tiles are done. What then becomes of a unit's state:
+// a time, and the rest to half as many more, which the SMs that are done first take.
+// A warp keeps its own ring of tiles in flight (cp.async), across the borders of units,
+// and waits for no other until its tiles are done. What then becomes of a unit's state:
 //   - all of its tiles in one warp: the warp writes the result;
 //   - it ends before the warp's last tile, having begun in an earlier warp: an end
 //     piece in the workspace, at the warp's number;
@@ -36,7 +36,7 @@
 //   weight times value the product of the two second terms (2^-11 of the weight, 2^-10
 //   of the value) is left out where it would take an instruction of its own.
 // Measured (held for half a second; the copy rate is 6.55 TB/s): 1M bf16 tokens of 4 KV
-// heads with 8 fp32 query heads each in 327 us (6.57 TB/s); 8 sequences up to 32K of 8
+// heads with 8 fp32 query heads each in 327 to 344 us by GPU (6.57 TB/s); 8 sequences up to 32K of 8
 // KV heads, 4 bf16 query heads each, in 98 us (6.15 TB/s, 94%); 160 ragged ones up to 3001
 // in 92 us (79%). A call starts to read after 3 us, the slowest SMs are done
 // some us after the mean, and the join takes 4 us, whatever the length. One
@@ -79,18 +79,17 @@ constexpr int kWideUnits = 148;
 inline int head_cols(int group) { return group > 8 ? 16 : group > 4 ? 8 : 4; }
 
 struct BatchLayout {
-  int64_t units, slots, bytes, slots_off;
+  int64_t slots, bytes, slots_off;
   int32_t hb, hu;                       // head blocks per KV head, heads per block
 };
 
-// Workspace: int64 prefix[n_seqs + 1] (tiles of one unit of the sequences
-// before s); then the group pieces and the end pieces, [m, l, 0, 0,
-// o[d]] for each of the unit's heads.
+// Workspace: int64 prefix[n_seqs + 1] (tiles of one unit of the sequences before s);
+// then the group pieces and the end pieces, [m, l, -, -, o[d]] for each of a unit's
+// heads.
 inline BatchLayout batch_layout(const Geom& G, int32_t n_seqs) {
   BatchLayout b{};
   b.hu = head_cols(G.group);
   b.hb = (G.group + b.hu - 1) / b.hu;
-  b.units = int64_t(n_seqs) * G.hkv * b.hb;
   b.slots = 2 * kMaxWarps;
   b.slots_off = round_up((int64_t(n_seqs) + 1) * 8, 256);
   b.bytes = b.slots_off + round_up(b.slots * b.hu * (G.d + 4) * 4, 256);

@@ -87,19 +87,6 @@ __host__ __device__ inline int64_t kv_row(const KvView& kv, int g, int64_t tok, 
   return int64_t(page) * chunk + (tok - c * chunk);
 }
 
-// Row of token `tok` of KV head g of sequence `seq` in a batch of caches (see
-// zha_attend_batch_kv), or -1. Rows fit 31 bits (checked on the host).
-__host__ __device__ inline int32_t kv_batch_row(const KvView& kv, int hkv, int seq, int g, int64_t tok,
-                                                int chunk) {
-  const int64_t head = int64_t(seq) * hkv + g;
-  if (kv.table == nullptr) return int32_t(head * kv.ld + tok);
-  const int64_t c = tok / chunk;
-  if (c >= kv.max_blocks) return -1;
-  const int32_t page = kv.table[head * kv.max_blocks + c];
-  if (page < 0 || int64_t(page) >= kv.ld) return -1;
-  return int32_t(int64_t(page) * chunk + (tok - c * chunk));
-}
-
 // C^l, saturating at a value above any token count.
 __host__ __device__ inline int64_t span_of(int32_t chunk, int32_t level) {
   int64_t s = 1;

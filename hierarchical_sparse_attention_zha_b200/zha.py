@@ -461,6 +461,14 @@ def _run_on(index: int, stream) -> int:
     return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, which is given back to that stream's later calls."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _status_ptr(status: torch.Tensor | None, index: int):
     if status is None:
         return None
@@ -529,7 +537,7 @@ def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor
         raise ValueError("x must be [T, heads, head_dim] of the rotation, float32 or bfloat16")
     on = _run_on(index, stream)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _new(shape, x.dtype, x.device, stream)
     to = _DTYPE.get(out.dtype)
     if to is None:
         raise ValueError("out must be float32 or bfloat16")
@@ -564,7 +572,7 @@ def rope_append_kv(cfg: Config, rope: Rope | None, q: torch.Tensor | None, k: to
     if q is not None:
         shape = (T, Hq, d)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=q_dtype, device=kv.device)
+            q_out = _new(shape, q_dtype, kv.device, stream)
         q_type = _DTYPE.get(q_out.dtype)
         if q_type is None or q_out.shape != shape or q_out.get_device() != dev or not q_out.is_contiguous():
             raise ValueError(f"q_out must be a contiguous float32 or bfloat16 tensor {list(shape)}")
@@ -600,15 +608,15 @@ def attend_batch_kv(cfg: Config, Q: torch.Tensor, kv: KvCache, n_seqs: int, n_to
     if dtype is None or Q.shape != want or Q.get_device() != dev or not Q.is_contiguous():
         raise ValueError(f"Q must be a contiguous float32 or bfloat16 tensor {list(want)} on the cache's device")
     if out is None:
-        out = torch.empty_like(Q)
+        out = _new(want, Q.dtype, kv.device, stream)
     elif out.shape != want or out.dtype is not Q.dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of Q's shape and type")
     if lse is None:
-        lse = torch.empty(want[:2], dtype=torch.float32, device=kv.device)
+        lse = _new(want[:2], torch.float32, kv.device, stream)
     elif lse.shape != want[:2] or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [n_seqs, Hq]")
     if ws is None:
-        ws = _bytes_tensor(attend_batch_workspace_bytes(cfg, n_seqs, max_tokens), kv.device)
+        ws = _new(max(1, attend_batch_workspace_bytes(cfg, n_seqs, max_tokens)), torch.uint8, kv.device, stream)
     st = lib.zha_attend_batch_kv(byref(cfg), Q.data_ptr(), dtype, byref(kv), n_seqs,
                                  _list_ptr(n_tokens, torch.int64, n_seqs, dev, "n_tokens"), max_tokens, out.data_ptr(),
                                  lse.data_ptr(), *_scratch(ws, dev), _status_ptr(status, dev), on)
@@ -641,7 +649,7 @@ def pages_extend(cfg: Config, pool: PagePool, seqs: torch.Tensor, n_tokens: torc
     n, dev = seqs.numel(), pool.index
     on = _run_on(dev, stream)
     if ws is None:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), pool.device)
+        ws = _new(max(1, pages_workspace_bytes(cfg, pool, n)), torch.uint8, pool.device, stream)
     st = lib.zha_pages_extend(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
                               _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
                               _status_ptr(status, dev), on)
@@ -656,7 +664,7 @@ def pages_fork(cfg: Config, pool: PagePool, src: torch.Tensor, dst: torch.Tensor
     n, dev = dst.numel(), pool.index
     on = _run_on(dev, stream)
     if ws is None:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, n), pool.device)
+        ws = _new(max(1, pages_workspace_bytes(cfg, pool, n)), torch.uint8, pool.device, stream)
     st = lib.zha_pages_fork(byref(cfg), byref(pool), _list_ptr(src, torch.int32, n, dev, "src"),
                             _list_ptr(dst, torch.int32, n, dev, "dst"),
                             _list_ptr(n_tokens, torch.int64, n, dev, "n_tokens"), n, *_scratch(ws, dev),
@@ -687,7 +695,7 @@ def pages_compact(cfg: Config, pool: PagePool, page_map: torch.Tensor | None = N
     dev = pool.index
     on = _run_on(dev, stream)
     if ws is None:
-        ws = _bytes_tensor(pages_workspace_bytes(cfg, pool, 0), pool.device)
+        ws = _new(max(1, pages_workspace_bytes(cfg, pool, 0)), torch.uint8, pool.device, stream)
     st = lib.zha_pages_compact(
         byref(cfg), byref(pool),
         None if page_map is None else _list_ptr(page_map, torch.int32, pool.shape[0], dev, "page_map"),

@@ -385,8 +385,7 @@ typedef struct {
  * y (y->data is written) may be x itself with the same type and strides, and must not
  * overlap x otherwise; its rows must lie apart, which is judged by the strides (the
  * smaller spans a row, the larger all rows of the other kind). Types are zha_dtype
- * values; the arithmetic is float32. n_tokens = 0
- * does nothing. */
+ * values; the arithmetic is float32. n_tokens = 0 does nothing. */
 zha_status zha_rope_apply(const zha_rope* rope, const zha_rows* x, int32_t x_dtype,
                           const int64_t* d_pos, int64_t n_tokens, int32_t n_heads, int32_t inverse,
                           const zha_rows* y, int32_t y_dtype, void* stream);
@@ -398,7 +397,7 @@ zha_status zha_rope_apply(const zha_rope* rope, const zha_rows* x, int32_t x_dty
  * turned the same way, to d_q_out [n_new][n_q_heads][head_dim] of type q_dtype,
  * as zha_route, zha_sparse_attend (float32) and zha_attend_batch_kv take them. rope
  * NULL: position-free keys, nothing is turned. kv->k and kv->v are written.
- *  - d_seq[t] < 0: padding; nothing of that token is read or written.
+ *  - d_seq[t] < 0: padding; nothing of that token is written (its rows may be read).
  *  - d_seq[t] >= n_seqs, or d_index[t] outside the table or ld: nothing of that token
  *    is written, ZHA_DEV_BAD_SEQUENCE. A table entry outside the pool: that
  *    head's key and value are not written, ZHA_DEV_BAD_PAGE.
@@ -424,10 +423,10 @@ zha_status zha_rope_append_kv(const zha_config* cfg, const zha_rope* rope, const
  * absent (ZHA_DEV_BAD_PAGE). Rows behind n are not read. Requires max_tokens <= ld, or
  * <= max_blocks * C. The split over the cache is made on the device from the counts,
  * so a captured call may be replayed with other counts. The workspace holds
- * nothing between calls; calls that may overlap need one each. A float32 result
- * is exact to float32 rounding for finite inputs (a bf16 cache's keys and values enter
- * exactly, queries and weights as three bf16 terms or two tf32 terms); with bf16
- * queries, weights are two bf16 terms. An infinity or NaN among the inputs makes the
+ * nothing between calls; calls that may overlap need one each. For finite inputs a
+ * float32 result has the error of float32 sums: over a bf16 cache every operand enters
+ * exactly, over a float32 cache within 2^-22; with bf16 queries weights enter within
+ * 2^-16. An infinity or NaN among the inputs makes the
  * results of its own head and sequence infinite or NaN, no others. */
 size_t zha_attend_batch_workspace_bytes(const zha_config* cfg, int32_t n_seqs, int64_t max_tokens);
 zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q_dtype,
@@ -461,8 +460,9 @@ typedef struct {
 size_t zha_pages_workspace_bytes(const zha_config* cfg, const zha_page_pool* pool, int32_t n_items);
 
 /* A page for every block without one among the first ceil(d_n_tokens[i] / C) blocks of
- * each KV head of sequence d_seqs[i]. All items or, when the free pages do
- * not suffice, none (ZHA_DEV_NO_PAGES). */
+ * each KV head of sequence d_seqs[i]. An item with an entry among them that names no
+ * page in use is refused (ZHA_DEV_BAD_PAGE). All other items or, when the free
+ * pages do not suffice, none (ZHA_DEV_NO_PAGES). */
 zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_seqs,
                             const int64_t* d_n_tokens, int32_t n_items, void* d_ws, size_t ws_bytes,
                             int32_t* d_status, void* stream);
@@ -470,10 +470,10 @@ zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, co
 /* Sequence d_dst[i] becomes a copy of the first d_n_tokens[i] tokens of d_src[i]:
  * full pages are shared (refs + 1), the rows in use of a part-filled last page are
  * copied to a page of its own, whose other rows stay as they were. One source may
- * serve many items. A destination must be empty (all entries < 0), no source may be
- * a destination of the same list, and the source's blocks must be pages in use
- * (else ZHA_DEV_BAD_PAGE); such an item is refused. All items that are not refused or,
- * without enough free pages, none (ZHA_DEV_NO_PAGES). */
+ * serve many items. Refused are an item whose destination is not empty (all entries
+ * < 0) or whose source is a destination of the same list (ZHA_DEV_BAD_SEQUENCE), and one
+ * whose source lacks a page in use for its tokens (ZHA_DEV_BAD_PAGE). All other items
+ * or, without enough free pages, none (ZHA_DEV_NO_PAGES). */
 zha_status zha_pages_fork(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_src,
                           const int32_t* d_dst, const int64_t* d_n_tokens, int32_t n_items, void* d_ws,
                           size_t ws_bytes, int32_t* d_status, void* stream);

@@ -322,6 +322,26 @@ def test_attend_two_calls_at_once(zha):
         assert torch.equal(o[0], want) and torch.equal(o[1], wlse)
 
 
+def test_memory_of_a_call_on_another_stream_is_that_streams(zha):
+    """A call given a stream takes its outputs and workspace from that stream's memory: a block
+    that the current stream's pending work still writes is not handed to it."""
+    b = Batch(zha, [3000, 7, 200], 2, 4, 64, 16, BF, F32, seed=19)
+    want, wlse = b.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for n in (want.numel() * 4, wlse.numel() * 4, zha.attend_batch_workspace_bytes(b.cfg, 3, b.most)):
+            late = torch.empty(n, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(2_000_000)
+            late.fill_(255)                       # still to come when the block is free again
+            del late
+        out, lse = b.run(stream=side)
+        side.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_batch_calls_refuse_another_calls_cache(zha):
     b = Batch(zha, [10], 1, 4, 64, 16, BF, F32, seed=18)
     tree_cache = zha.kv_cache(b.K, b.V, b.table[0].contiguous())       # one sequence's, without what is checked here
