@@ -63,6 +63,10 @@ constexpr int kMaxWarps = kMaxCtas * kWarps;
 // the reads, take the time (12 heads: 143 with it, 135 without). An eighth to as many
 // CTAs as in the first: 105 and 95; a sixteenth to half as many 102 and 93.
 constexpr int kTwoTiers = 24;
+// What a unit's start and end cost, in tiles: the deal counts them, so that a warp with
+// many short units has fewer tiles (238 sequences up to 255 tokens of 8 KV heads: 33.7 us,
+// 53.5 without; 1 37.2, 5 34.7).
+constexpr int kUnitCost = 2;
 constexpr int kMinTiles = 2;            // no warp takes less, unless there is less
 // Up to so many tiles a unit, and no more units than CTAs at a time, a CTA takes a
 // whole unit and no second kernel is needed (64 sequences of 500 tokens and 4 heads:
@@ -72,6 +76,7 @@ constexpr int kJoinThreads = 256;
 // Up to so many units, each in many pieces, a CTA joins one head, else one unit (60K
 // tokens in 4 units: 31.1 us, 36.9 by units).
 constexpr int kWideUnits = 148;
+constexpr int join_units(int hu) { return kJoinThreads / 32 / (hu / 4); }   // of a CTA otherwise
 
 // Heads a unit: the fewest columns that take the group (8 x 32K tokens of 4 heads: 102.5
 // us with 4 columns and two terms side by side, 104.4 with 8; of 12 heads 142.9 with
@@ -106,7 +111,7 @@ struct BatchArgs {
   int64_t* prefix;
   float* slots;
   int32_t* status;
-  int32_t n_seqs, hkv, hq, group, hb, chunk, single;
+  int32_t n_seqs, hkv, hq, group, hb, chunk, single, wide;
   int32_t first_ctas, ctas;             // of the first deal, of both
   uint32_t div_mul, div_shift;          // t / chunk = t * div_mul >> div_shift for t < 2^31
   float scale_log2;                     // log2(e) / sqrt(d)
@@ -199,7 +204,7 @@ struct Tile {
 };
 
 // A place in the row of tiles: unit (s, ub) of sequence s with n tokens has the
-// tiles [first, end).
+// tiles [first, end), behind kUnitCost places that stand for its start and end.
 struct Place {
   int64_t first, end, n;
   int s, ub;
@@ -210,6 +215,9 @@ __device__ __forceinline__ int64_t clamped(const BatchArgs& A, int s) {
 }
 template <int KEYS>
 __device__ __forceinline__ int64_t tiles_of(int64_t n) { return (n + KEYS - 1) / KEYS; }
+// A unit's places in the row.
+template <int KEYS>
+__device__ __forceinline__ int64_t places_of(int64_t n) { return n == 0 ? 0 : kUnitCost + (n + KEYS - 1) / KEYS; }
 
 // (The hardware has no integer division: 32-bit ones take a fifth of the 64-bit ones.)
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -253,8 +261,8 @@ __device__ __forceinline__ void next_unit(const BatchArgs& A, Place& p) {
     p.ub = 0;
     do p.n = clamped(A, ++p.s); while (p.n == 0);
   }
-  p.first = p.end;
-  p.end += tiles_of<KEYS>(p.n);
+  p.first = p.end + kUnitCost;
+  p.end = p.first + tiles_of<KEYS>(p.n);
 }
 
 // What a lane (g, t) = (lane / 4, lane % 4) has of the columns: 2 t and 2 t + 1 of a
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
     const int run = (A.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(A.n_seqs, tid * run), s1 = min(A.n_seqs, s0 + run);
     int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += tiles_of<KEYS>(clamped(A, s));
+    for (int s = s0; s < s1; ++s) mine += places_of<KEYS>(clamped(A, s));
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -599,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) starts[w] = deal.start(w0 + w);
     for (int s = s0; s < s1; ++s) {
-      const int64_t n = A.n_tokens[s], tl = tiles_of<KEYS>(clamped(A, s));
+      const int64_t n = A.n_tokens[s], tl = places_of<KEYS>(clamped(A, s));
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         if (starts[w] >= at * per && starts[w] < (at + tl) * per) { J.at[w][0] = s; J.at[w][1] = at; }
@@ -617,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
     if (t0 < t1) {
       cur.s = int(J.at[warp][0]);
       cur.n = clamped(A, cur.s);
-      const int64_t tl = tiles_of<KEYS>(cur.n), base = J.at[warp][1] * per;
+      const int64_t tl = places_of<KEYS>(cur.n), base = J.at[warp][1] * per;
       cur.ub = int(quotient(t0 - base, tl));
-      cur.first = base + cur.ub * tl;
-      cur.end = cur.first + tl;
+      cur.end = base + (cur.ub + 1) * tl;
+      cur.first = cur.end - tl + kUnitCost;
     }
   }
 
@@ -637,6 +645,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       next_unit<KEYS>(A, ahead);
       head = int64_t(ahead.s) * A.hkv + ahead.ub / A.hb;
     }
+    next = max64(next, ahead.first);
+    if (next >= t1) return;
     const int64_t tok = (next - ahead.first) * KEYS + lane;
     if (lane < KEYS && tok < ahead.n) {
       const uint32_t t = uint32_t(tok);
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-  int64_t at = t0;
+  int64_t at = t0 < t1 ? max64(t0, cur.first) : t1;
   int stage = 0;
   float m[NQ][2], l[NQ][2], o[NQ][D / 16][4];
   const bool mine = HU != 4 || t4 < 2;                       // of two lanes with the same heads
@@ -810,7 +820,10 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
       J.starts[warp] = starts;
       J.ends[warp] = ends;
     }
-    if (at < t1) next_unit<KEYS>(A, cur);
+    if (at < t1) {
+      next_unit<KEYS>(A, cur);
+      at = max64(at, cur.first);
+    }
   }
 
   // The open states, joined where neighbouring warps have the same unit. The rings
@@ -863,17 +876,19 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
 
 // A unit's pieces joined: nothing to do for a finished unit; zeros for one without
 // tiles. Grid (units, heads): one CTA a head, its pieces dealt to the warps (few
-// units, many pieces each). Grid (units, 1): one warp a head.
+// units, many pieces each). Grid (units / kUnits, 1): one warp for 4 heads of a unit.
 template <typename Qt, int D, int HU>
 __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const BatchArgs A) {
-  constexpr int EPL = D / 32, kJoinWarps = kJoinThreads / 32;
+  constexpr int EPL = D / 32, kJoinWarps = kJoinThreads / 32, kUnits = join_units(HU);
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const bool wide = gridDim.y > 1;
+  const bool wide = A.wide != 0;
   const int split = wide ? kJoinWarps : 1, part = wide ? warp : 0;
   pdl_trigger();
   pdl_wait();
-  const int per = A.hkv * A.hb, s = blockIdx.x / per, ub = blockIdx.x - s * per;
+  const int per = A.hkv * A.hb, unit = wide ? blockIdx.x : blockIdx.x * kUnits + warp % kUnits;
+  const int s = unit / per, ub = unit - s * per;
+  if (s >= A.n_seqs) return;
   const int heads = min(HU, A.group - (ub % A.hb) * HU);
   const int64_t row0 = int64_t(s) * A.hq + int64_t(ub / A.hb) * A.group + (ub % A.hb) * HU;
   const int64_t seq_tile = A.prefix[s], tl = A.prefix[s + 1] - seq_tile;
@@ -883,7 +898,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const B
     // Warps w0..w1 have the unit; the last one's state is an end piece unless the unit
     // ends with that warp's tiles.
     const Deal deal(A, total);
-    const int64_t lo = seq_tile * per + ub * tl, hi = lo + tl;
+    const int64_t hi = seq_tile * per + (ub + 1) * tl, lo = hi - tl + kUnitCost;
     w0 = int(deal.owner(lo));
     w1 = int(deal.owner(hi - 1));
     const bool apart = hi != deal.start(w1 + 1);
@@ -891,7 +906,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const B
     n = groups + apart;
     if (w0 == w1 || n == 1) return;
   }
-  for (int h = wide ? blockIdx.y : warp; h < heads; h += kJoinWarps) {
+  const int h0 = wide ? blockIdx.y : warp / kUnits * 4, h1 = wide ? h0 + 1 : min(heads, h0 + 4);
+  for (int h = h0; h < min(heads, h1); ++h) {
     // Pieces in rounds of 8, all of a round's loads before its arithmetic.
     float M = -INFINITY, L = 0.f, acc[EPL] = {};
     for (int i0 = part; i0 < n; i0 += 8 * split) {
@@ -970,7 +986,7 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   const int64_t tiles = (A.max_tokens + Tile<Kv, D>::kKeys - 1) / Tile<Kv, D>::kKeys;
   A.single = tiles <= kSingleTiles && units <= int64_t(sms) * 2;
   sms = sms < kMaxSms ? sms : kMaxSms;
-  const int64_t most = units * tiles;
+  const int64_t most = units * (tiles + kUnitCost);
   A.first_ctas = int32_t(max64(1, min64(sms * 2, (most + kWarps * kMinTiles - 1) / (kWarps * kMinTiles))));
   A.ctas = HU < 16 && most >= int64_t(kTwoTiers) * kWarps * sms * 2 ? sms * 3 : A.first_ctas;
   const int64_t ctas = A.single ? units : A.ctas;
@@ -983,7 +999,10 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   if (A.single) return cudaSuccess;
   TraceScope ts("attend_batch_join_kernel", 0, s);
   zha_count_launch();
-  return launch_pdl(attend_batch_join_kernel<Qt, D, HU>, dim3(unsigned(units), unsigned(units <= kWideUnits ? min64(HU, A.group) : 1)), dim3(kJoinThreads), 0, s, A);
+  A.wide = units <= kWideUnits;
+  const dim3 grid = A.wide ? dim3(unsigned(units), unsigned(min64(HU, A.group)))
+                           : dim3(unsigned((units + join_units(HU) - 1) / join_units(HU)));
+  return launch_pdl(attend_batch_join_kernel<Qt, D, HU>, grid, dim3(kJoinThreads), 0, s, A);
 }
 
 template <typename Kv, typename Qt>

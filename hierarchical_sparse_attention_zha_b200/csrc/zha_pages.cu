@@ -31,7 +31,10 @@ constexpr int kPageThreads = 256;         // of the kernels over the whole GPU
 constexpr int kBookThreads = 1024;        // of the cluster's CTAs
 constexpr int kBookWarps = kBookThreads / 32;
 constexpr int kMostCtas = 16;
-constexpr int64_t kCopyHere = 256 << 10;  // bytes the cluster copies itself (a beam of 4: 20.0 us, 20.5 and a launch without)
+// The cluster copies a fork's part-filled pages itself where a warp's page is small, and
+// all of them together (a beam of 4, 4 KB of K a page: 20.0 us, 20.5 and a launch
+// without; 32 KB of K a page: 33 us, 22 without). Compact: twice the bytes.
+constexpr int64_t kCopyHere = 256 << 10, kCopyPage = 4096;
 
 struct PoolArgs {
   char* k;
@@ -571,7 +574,8 @@ zha_status run_items(const PoolArgs& P, const int32_t* src, const int32_t* dst, 
   const PageWs W = page_ws(d_ws, P.n_pages, rows);
   zha_status st = need_ws(d_ws, ws_bytes, W.bytes);
   if (st != ZHA_OK) return st;
-  const bool copy_here = rows * P.chunk * P.row_bytes <= kCopyHere;
+  const int64_t page_bytes = int64_t(P.chunk) * P.row_bytes;
+  const bool copy_here = page_bytes <= kCopyPage && rows * page_bytes <= kCopyHere;
   st = launch_book("pages_items_kernel", who, pages_items_kernel<kFork>, P, rows, s, P, W, src, dst, tokens, n_items,
                    copy_here);
   if (st != ZHA_OK || !kFork || copy_here) return st;
