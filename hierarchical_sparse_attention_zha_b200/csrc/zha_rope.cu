@@ -13,9 +13,10 @@
 // than 2^-28.
 //
 // A row is read in pieces of 8 elements, two a lane: the two that hold the elements of
-// 8 pairs, so that a lane turns what it has read. (Half layout with an odd split: two
-// adjacent pieces, and the pairs' other elements once more, one by one.) A block makes
-// the cosines and sines of its tokens once, while its first rows are on their way.
+// 8 pairs, so that a lane turns what it has read. (Half layout with a split inside a
+// piece: two adjacent pieces, and the pairs' other elements through shared memory.) A
+// block makes the cosines and sines of its tokens once, while its first rows are on
+// their way.
 //
 // Bound: HBM, each row read once and written once; the launch for few tokens. Measured
 // (the copy rate is 6.55 TB/s): 32K tokens x 32 bf16 rows of 128 in 89 us (6.0 TB/s, 92%);
@@ -118,8 +119,17 @@ int mode_of(const RopeTable& R) { return !R.half ? kOwn : R.pairs % 8 == 0 ? kPa
 // take two pairs of their 8 at a time, read adjacent 16 bytes.
 template <int MODE>
 __device__ __forceinline__ int turn_slot(int p) {
-  return MODE == kAcross ? p : ((p % 8 / 2) * 8 + p / 8) * 2 + p % 2;
+  return MODE == kAcross ? p + p / 16 : ((p % 8 / 2) * 8 + p / 8) * 2 + p % 2;
 }
+constexpr int kTurns = 64 + 4;           // places of a token's turns
+
+// For kAcross a warp's rows pass through shared memory, element e at e + e / 16, so that
+// the lanes, 16 elements apart, and the rows meet no bank twice.
+constexpr int row_floats(int d) { return d + d / 16; }
+template <int D, int MODE>
+struct RowBuffer {
+  float x[MODE == kAcross ? kRopeWarps : 1][MODE == kAcross ? 512 / D * row_floats(D) : 1];
+};
 
 // What a lane does with its two pieces (from elements a0 and b0 on) of every row.
 template <int D, int MODE>
@@ -133,9 +143,8 @@ struct Lane {
     on = MODE == kPair ? pair : MODE == kOwn ? unit * 8 < P : a0 < 2 * P;
   }
 
-  // The pieces a and b of a row, turned. For kAcross elements are read once more.
-  template <typename T>
-  __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* cs, const T* row, int P) const {
+  // The pieces a and b of a row, turned. For kAcross `row` is the row in shared memory.
+  __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* cs, const float* row, int P) const {
     const float4* two = reinterpret_cast<const float4*>(cs);
     if constexpr (MODE == kPair) {
 #pragma unroll
@@ -164,13 +173,20 @@ struct Lane {
         }
       }
     } else {
+      // Element a0 + i's place is 17 unit + i; that of an element `by` further on 17 unit
+      // + (i + by) + floor((i + by) / 16), with the same step for all lanes.
+      const float* mine = row + unit * 17;
+      const float2* turns = cs + unit * 17;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int e = a0 + i;
-        if (e >= 2 * P) break;
+        const int up = i + P, down = i - P;
+        if (a0 + i >= 2 * P) break;
+        const bool first = a0 + i < P;
         float& v = i < 8 ? a[i & 7] : b[i & 7];
-        const float2 t = cs[e < P ? e : e - P];
-        v = v * t.x + float(row[e < P ? e + P : e - P]) * (e < P ? -t.y : t.y);
+        const int down_at = down + (down >> 4);
+        const float2 t = turns[first ? i : down_at];
+        const float w = mine[first ? up + (up >> 4) : down_at];
+        v = v * t.x + w * (first ? -t.y : t.y);
       }
     }
   }
@@ -195,7 +211,7 @@ struct Row {
 // destination `to`, asked for a batch at a time; rows from `plain` on are not turned.
 // ready() runs while the first batch is on its way, and ends with the block in step.
 template <int D, int MODE, typename Src, typename Where, typename Ready, typename Target, typename Store>
-__device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const float2 (*cs)[64], int P, int plain,
+__device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const float2 (*cs)[kTurns], RowBuffer<D, MODE>& rows_in, int P, int plain,
                                           Where where, Ready ready, Target target, Store store) {
   constexpr int kPer = 512 / D;                               // rows a warp reads at a time
   constexpr int kRows = 2;                                    // a lane has in flight
@@ -236,8 +252,18 @@ __device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const f
         float a[8], b[8];
         x[k].get(a);
         y[k].get(b);
-        if (here && turned) mine.turn(a, b, cs[t], row.at + t * row.token, P);
-        if (MODE == kAcross) __syncwarp();                   // a row in place is read before it is written
+        float* through = rows_in.x[MODE == kAcross ? warp : 0];
+        if constexpr (MODE == kAcross) {
+          through += lane / (D / 16) * row_floats(D);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            through[mine.unit * 17 + i] = a[i];
+            through[mine.unit * 17 + 8 + i] = b[i];
+          }
+          __syncwarp();
+        }
+        if (here && turned) mine.turn(a, b, cs[t], through, P);
+        if constexpr (MODE == kAcross) __syncwarp();         // read before the next row is put there
         if (here) {
           store(r, mine.a0, a, to[k]);
           store(r, mine.b0, b, to[k]);
@@ -249,7 +275,7 @@ __device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const f
 
 // Cosines and sines of `have` tokens from t0 on.
 template <int MODE>
-__device__ __forceinline__ void fill_turns(const RopeTable& R, float2 (*cs)[64], const int64_t* pos, int have, bool back) {
+__device__ __forceinline__ void fill_turns(const RopeTable& R, float2 (*cs)[kTurns], const int64_t* pos, int have, bool back) {
   for (int i = threadIdx.x; i < have * 64; i += kRopeThreads)
     if (i % 64 < R.pairs) cs[i / 64][turn_slot<MODE>(i % 64)] = cos_sin_of(R.turn[i % 64], pos[i / 64], R.amplitude, back);
 }
@@ -259,7 +285,8 @@ template <typename Src, typename Dst, int D, int MODE>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(Src) == 2 ? 4 : 3)
     rope_apply_kernel(const __grid_constant__ RopeTable R, RowSet X, const int64_t* pos, int64_t n_tokens, RowPlan plan,
                       int back) {
-  __shared__ __align__(16) float2 cs[kRopeTokens][64];
+  __shared__ __align__(16) float2 cs[kRopeTokens][kTurns];
+  __shared__ RowBuffer<D, MODE> rows_in;
   pdl_trigger();
   pdl_wait();
   for (int64_t t0 = int64_t(blockIdx.x) * plan.tokens; t0 < n_tokens; t0 += int64_t(gridDim.x) * plan.tokens) {
@@ -267,7 +294,7 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(Src) == 2 ? 4 : 3)
     const Src* src = static_cast<const Src*>(X.src) + t0 * X.src_token;
     Dst* dst = static_cast<Dst*>(X.dst) + t0 * X.dst_token;
     turn_rows<D, MODE, Src>(
-        plan, have, cs, R.pairs, X.heads, [&](int r) { return Row<Src>{src + r * X.src_head, X.src_token}; },
+        plan, have, cs, rows_in, R.pairs, X.heads, [&](int r) { return Row<Src>{src + r * X.src_head, X.src_token}; },
         [&] {
           __syncthreads();
           fill_turns<MODE>(R, cs, pos + t0, have, back != 0);
@@ -283,7 +310,8 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(Src) == 2 ? 4 : 3)
     rope_append_kernel(const __grid_constant__ RopeTable R, RowSet Q, RowSet K, RowSet V, KvView kv, int n_seqs,
                        const int32_t* seq, const int64_t* index, const int64_t* pos, int64_t n_new, RowPlan plan, int chunk,
                        int32_t* status) {
-  __shared__ __align__(16) float2 cs[kRopeTokens][64];
+  __shared__ __align__(16) float2 cs[kRopeTokens][kTurns];
+  __shared__ RowBuffer<D, MODE> rows_in;
   // Of each token, for its first KV head (-1: nothing is written): the table's entry
   // and the place in the page; in a contiguous cache the row.
   __shared__ int64_t s_at[kRopeTokens];
@@ -298,7 +326,7 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(Src) == 2 ? 4 : 3)
     const Src* k = static_cast<const Src*>(K.src) + t0 * K.src_token;
     const Src* v = static_cast<const Src*>(V.src) + t0 * V.src_token;
     turn_rows<D, MODE, Src>(
-        plan, have, cs, R.pairs, R.pairs > 0 ? hq + hkv : 0,
+        plan, have, cs, rows_in, R.pairs, R.pairs > 0 ? hq + hkv : 0,
         [&](int r) {
           return r < hq         ? Row<Src>{q + r * Q.src_head, Q.src_token}
                  : r < hq + hkv ? Row<Src>{k + (r - hq) * K.src_head, K.src_token}
