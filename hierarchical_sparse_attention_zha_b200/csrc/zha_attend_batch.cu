@@ -36,12 +36,11 @@
 //   weight times value the product of the two second terms (2^-11 of the weight, 2^-10
 //   of the value) is left out where it would take an instruction of its own.
 // Measured (held for half a second; the copy rate is 6.55 TB/s): 1M bf16 tokens of 4 KV
-// heads with 8 fp32 query heads each in 327 to 344 us by GPU (6.57 TB/s); 8 sequences up to 32K of 8
-// KV heads, 4 bf16 query heads each, in 98 us (6.15 TB/s, 94%); 160 ragged ones up to 3001
-// in 92 us (79%). A call starts to read after 3 us, the slowest SMs are done
-// some us after the mean, and the join takes 4 us, whatever the length. One
-// bulk copy per row instead of 16 cp.async of 16 bytes: 495 us for the 1M tokens, 17
-// cycles of an SM each.
+// heads with 8 fp32 query heads each in 327 to 346 us by GPU (6.2 to 6.57 TB/s); 8
+// sequences up to 32K of 8 KV heads, 4 bf16 query heads each, in 98 to 102 us (91 to 94%);
+// 160 ragged ones up to 3001 in 90 us (80%). A call starts to read after 3 us, and the
+// join takes 3 to 4 us, whatever the length. One bulk copy per row instead of 16 cp.async
+// of 16 bytes: 495 us for the 1M tokens, 17 cycles of an SM each.
 #include <cmath>
 
 #include "zha_host.cuh"
@@ -76,7 +75,9 @@ constexpr int kJoinThreads = 256;
 // Up to so many units, each in many pieces, a CTA joins one head, else one unit (60K
 // tokens in 4 units: 31.1 us, 36.9 by units).
 constexpr int kWideUnits = 148;
-constexpr int join_units(int hu) { return kJoinThreads / 32 / (hu / 4); }   // of a CTA otherwise
+// A unit's warps otherwise, two heads each (160 ragged sequences of 4 heads a unit: 89.3
+// us, 91.7 with 4 heads each).
+__host__ __device__ constexpr int join_warps_of(int hu, int group) { return ((group < hu ? group : hu) + 1) / 2; }
 
 // Heads a unit: the fewest columns that take the group (8 x 32K tokens of 4 heads: 102.5
 // us with 4 columns and two terms side by side, 104.4 with 8; of 12 heads 142.9 with
@@ -876,19 +877,20 @@ __global__ void __launch_bounds__(kThreads, 2) attend_batch_kernel(const BatchAr
 
 // A unit's pieces joined: nothing to do for a finished unit; zeros for one without
 // tiles. Grid (units, heads): one CTA a head, its pieces dealt to the warps (few
-// units, many pieces each). Grid (units / kUnits, 1): one warp for 4 heads of a unit.
+// units, many pieces each). Otherwise one warp for two heads of a unit.
 template <typename Qt, int D, int HU>
 __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const BatchArgs A) {
-  constexpr int EPL = D / 32, kJoinWarps = kJoinThreads / 32, kUnits = join_units(HU);
+  constexpr int EPL = D / 32, kJoinWarps = kJoinThreads / 32;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool wide = A.wide != 0;
   const int split = wide ? kJoinWarps : 1, part = wide ? warp : 0;
   pdl_trigger();
   pdl_wait();
-  const int per = A.hkv * A.hb, unit = wide ? blockIdx.x : blockIdx.x * kUnits + warp % kUnits;
+  const int per = A.hkv * A.hb, join_warps = join_warps_of(HU, A.group);
+  const int in_cta = kJoinWarps / join_warps, unit = wide ? blockIdx.x : blockIdx.x * in_cta + warp / join_warps;
   const int s = unit / per, ub = unit - s * per;
-  if (s >= A.n_seqs) return;
+  if (s >= A.n_seqs || (!wide && warp >= in_cta * join_warps)) return;
   const int heads = min(HU, A.group - (ub % A.hb) * HU);
   const int64_t row0 = int64_t(s) * A.hq + int64_t(ub / A.hb) * A.group + (ub % A.hb) * HU;
   const int64_t seq_tile = A.prefix[s], tl = A.prefix[s + 1] - seq_tile;
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_batch_join_kernel(const B
     n = groups + apart;
     if (w0 == w1 || n == 1) return;
   }
-  const int h0 = wide ? blockIdx.y : warp / kUnits * 4, h1 = wide ? h0 + 1 : min(heads, h0 + 4);
+  const int h0 = wide ? blockIdx.y : warp % join_warps * 2, h1 = wide ? h0 + 1 : h0 + 2;
   for (int h = h0; h < min(heads, h1); ++h) {
     // Pieces in rounds of 8, all of a round's loads before its arithmetic.
     float M = -INFINITY, L = 0.f, acc[EPL] = {};
@@ -1000,8 +1002,9 @@ cudaError_t launch_batch(BatchArgs A, cudaStream_t s) {
   TraceScope ts("attend_batch_join_kernel", 0, s);
   zha_count_launch();
   A.wide = units <= kWideUnits;
+  const int64_t in_cta = kJoinThreads / 32 / join_warps_of(HU, A.group);
   const dim3 grid = A.wide ? dim3(unsigned(units), unsigned(min64(HU, A.group)))
-                           : dim3(unsigned((units + join_units(HU) - 1) / join_units(HU)));
+                           : dim3(unsigned((units + in_cta - 1) / in_cta));
   return launch_pdl(attend_batch_join_kernel<Qt, D, HU>, grid, dim3(kJoinThreads), 0, s, A);
 }
 
