@@ -1049,12 +1049,14 @@ zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q
   zha::BatchArgs A{};
   if ((st = zha_batch_view(G, kv, n_seqs, max_tokens, who, &A.kv)) != ZHA_OK) return st;
   if (!aligned16(d_Q) || !aligned16(d_O))
-    return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: Q and O must be non-NULL 16-byte aligned device pointers");
+    return zha_report_error(ZHA_ERR_INVALID,
+                            "zha_attend_batch_kv: Q and O must be non-NULL 16-byte aligned device pointers");
   if (q_dtype != ZHA_F32 && q_dtype != ZHA_BF16)
     return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: unknown q_dtype");
   if (d_n_tokens == nullptr) return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: n_tokens is NULL");
   if (!zha::units_ok(G, n_seqs))
-    return zha_report_error(ZHA_ERR_UNSUPPORTED, "zha_attend_batch_kv: more than 2^22 (sequence, KV head, query block) units");
+    return zha_report_error(ZHA_ERR_UNSUPPORTED,
+                            "zha_attend_batch_kv: more than 2^22 (sequence, KV head, query block) units");
   const zha::BatchLayout lay = zha::batch_layout(G, n_seqs);
   if (d_ws == nullptr || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0 || int64_t(ws_bytes) < lay.bytes)
     return zha_report_error(ZHA_ERR_CAPACITY,

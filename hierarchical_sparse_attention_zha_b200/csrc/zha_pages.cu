@@ -32,8 +32,9 @@ constexpr int kBookThreads = 1024;        // of the cluster's CTAs
 constexpr int kBookWarps = kBookThreads / 32;
 constexpr int kMostCtas = 16;
 // The cluster copies a fork's part-filled pages itself where a warp's page is small, and
-// all of them together (a beam of 4, 4 KB of K a page: 20.0 us, 20.5 and a launch
-// without; 32 KB of K a page: 33 us, 22 without). Compact: twice the bytes.
+// all of them together (a beam step of 4, 4 KB of K a page: 20.0 us on the device, without
+// 20.5 and a launch more; 32 KB of K a page: 38.9 us, 24.9 without). Compact: twice the
+// bytes.
 constexpr int64_t kCopyHere = 256 << 10, kCopyPage = 4096;
 
 struct PoolArgs {
@@ -604,7 +605,8 @@ zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, co
   PoolArgs P;
   zha_status st = zha::pool_args(cfg, pool, "zha_pages_extend", &P);
   if (st != ZHA_OK) return st;
-  if ((st = zha::items_ok(P, n_items, d_seqs, d_n_tokens, "zha_pages_extend: n_items out of range, or seqs or n_tokens NULL")) != ZHA_OK || n_items == 0)
+  if ((st = zha::items_ok(P, n_items, d_seqs, d_n_tokens,
+                          "zha_pages_extend: n_items out of range, or seqs or n_tokens NULL")) != ZHA_OK || n_items == 0)
     return st;
   P.status = d_status;
   return zha::run_items<false>(P, nullptr, d_seqs, d_n_tokens, n_items, d_ws, ws_bytes,
@@ -617,7 +619,8 @@ zha_status zha_pages_fork(const zha_config* cfg, const zha_page_pool* pool, cons
   PoolArgs P;
   zha_status st = zha::pool_args(cfg, pool, "zha_pages_fork", &P);
   if (st != ZHA_OK) return st;
-  if ((st = zha::items_ok(P, n_items, d_dst, d_n_tokens, "zha_pages_fork: n_items out of range, or dst or n_tokens NULL")) != ZHA_OK || n_items == 0)
+  if ((st = zha::items_ok(P, n_items, d_dst, d_n_tokens,
+                          "zha_pages_fork: n_items out of range, or dst or n_tokens NULL")) != ZHA_OK || n_items == 0)
     return st;
   if (d_src == nullptr) return zha_report_error(ZHA_ERR_INVALID, "zha_pages_fork: src is NULL");
   P.status = d_status;
@@ -630,7 +633,8 @@ zha_status zha_pages_free(const zha_config* cfg, const zha_page_pool* pool, cons
   PoolArgs P;
   zha_status st = zha::pool_args(cfg, pool, "zha_pages_free", &P);
   if (st != ZHA_OK) return st;
-  if ((st = zha::items_ok(P, n_items, d_seqs, d_seqs, "zha_pages_free: n_items out of range, or seqs NULL")) != ZHA_OK || n_items == 0)
+  if ((st = zha::items_ok(P, n_items, d_seqs, d_seqs,
+                          "zha_pages_free: n_items out of range, or seqs NULL")) != ZHA_OK || n_items == 0)
     return st;
   P.status = d_status;
   return zha::launch_page_kernel("pages_free_kernel", "zha_pages_free", zha::pages_free_kernel,

@@ -212,8 +212,9 @@ struct Row {
 // destination `to`, asked for a batch at a time; rows from `plain` on are not turned.
 // ready() runs while the first batch is on its way, and ends with the block in step.
 template <int D, int MODE, typename Src, typename Where, typename Ready, typename Target, typename Store>
-__device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const float2 (*cs)[kTurns], RowBuffer<D, MODE>& rows_in, int P, int plain,
-                                          Where where, Ready ready, Target target, Store store) {
+__device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const float2 (*cs)[kTurns],
+                                          RowBuffer<D, MODE>& rows_in, int P, int plain, Where where, Ready ready,
+                                          Target target, Store store) {
   constexpr int kPer = 512 / D;                               // rows a warp reads at a time
   constexpr int kRows = 2;                                    // a lane has in flight
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -276,7 +277,8 @@ __device__ __forceinline__ void turn_rows(const RowPlan& plan, int have, const f
 
 // Cosines and sines of `have` tokens from t0 on.
 template <int MODE>
-__device__ __forceinline__ void fill_turns(const RopeTable& R, float2 (*cs)[kTurns], const int64_t* pos, int have, bool back) {
+__device__ __forceinline__ void fill_turns(const RopeTable& R, float2 (*cs)[kTurns], const int64_t* pos, int have,
+                                           bool back) {
   for (int i = threadIdx.x; i < have * 64; i += kRopeThreads)
     if (i % 64 < R.pairs) cs[i / 64][turn_slot<MODE>(i % 64)] = cos_sin_of(R.turn[i % 64], pos[i / 64], R.amplitude, back);
 }
