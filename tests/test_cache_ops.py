@@ -306,6 +306,19 @@ def test_attend_captured_replayed_with_other_counts_and_streams(zha):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("lens", [[300, 0, 17], [90000, 0, 17]])
+def test_attend_without_lse_or_status(zha, lens):
+    """The C call with the results that may be left out left out: short units, and split ones."""
+    from ctypes import byref
+    b = Batch(zha, lens, 1, 4, 64, 16, BF, F32, seed=21)
+    want, _ = b.run()
+    out = torch.full_like(b.Q, 9.0)
+    ws = torch.empty(zha.attend_batch_workspace_bytes(b.cfg, 3, b.most), dtype=torch.uint8, device="cuda")
+    rc = zha.lib.zha_attend_batch_kv(byref(b.cfg), b.Q.data_ptr(), zha.ZHA_F32, byref(b.kv), 3, b.n.data_ptr(), b.most,
+                                     out.data_ptr(), None, ws.data_ptr(), ws.numel(), None, zha.stream_ptr())
+    assert rc == zha.ZHA_OK and torch.equal(out, want)
+
+
 def test_attend_two_calls_at_once(zha):
     """Two streams, a workspace each, over one cache."""
     b = Batch(zha, [40000, 7, 20000], 2, 4, 64, 16, BF, F32, seed=17)
@@ -839,6 +852,22 @@ def test_pages_long_lists(zha):
     assert p.extend(twice, [6] * 3000 + [2]) == zha.ZHA_DEV_BAD_SEQUENCE
     p.compact()
     assert p.extend(order, [6] * S) in (0, zha.ZHA_DEV_NO_PAGES)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_pages_with_counts_at_any_word(zha, shift):
+    """Reference counts that start between 16-byte boundaries, and a table too."""
+    p = Pages(zha, 7, 2, 4, 6, 9001, seed=8)
+    p.refs = torch.zeros(9001 + shift, dtype=torch.int32, device="cuda")[shift:]
+    p.table = torch.full((7 * 2 * 6 + shift,), -1, dtype=torch.int32, device="cuda")[shift:].view(7, 2, 6)
+    p.pool = zha.page_pool(p.K, p.V, p.table, p.refs)
+    p.r[:] = np.arange(9001) % 3 == 0             # a third in use by no one listed here
+    p.put()
+    assert p.extend([0, 3, 5], [24, 9, 1]) == 0
+    assert p.fork([0, 3], [1, 2], [22, 9]) == 0
+    assert p.free([0], [5]) == 0
+    assert p.compact() == 0
+    assert p.extend(list(range(7)), [24] * 7) == 0
 
 
 def test_pages_captured_with_one_workspace(zha):
