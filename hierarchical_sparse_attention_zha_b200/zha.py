@@ -499,11 +499,12 @@ def _row_args(x: torch.Tensor, shape: tuple, index: int, name: str) -> tuple[int
     return x.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
-def _same_cache(cfg: Config, c) -> None:
-    """A configuration and a kv_batch() or page_pool() that describe one cache."""
+def _same_cache(cfg: Config, c, kind: type) -> None:
+    """A configuration and a kv_batch() (kind KvCache) or page_pool() (kind PagePool) that
+    describe one cache. The two have C structs of different sizes: one for the other is refused."""
     s = getattr(c, "shape", None)
-    if s is None:
-        raise ValueError("the cache must come from kv_batch() or page_pool()")
+    if s is None or not isinstance(c, kind):
+        raise ValueError("the cache must come from " + ("kv_batch()" if kind is KvCache else "page_pool()"))
     if (c.heads != cfg.n_kv_heads or s[-1] != cfg.head_dim or c.dtype != cfg.kv_dtype
             or (len(s) == 3 and s[1] != cfg.chunk)):
         raise ValueError("the cache does not match the configuration")
@@ -560,7 +561,7 @@ def rope_append_kv(cfg: Config, rope: Rope | None, q: torch.Tensor | None, k: to
     """zha_rope_append_kv: k, v [T, Hkv, d] into the caches of kv_batch() at row index[t] of
     sequence seq[t], keys turned at pos (None: index); q [T, Hq, d] turned into q_out, which
     is returned (None without q). rope None: nothing is turned."""
-    _same_cache(cfg, kv)
+    _same_cache(cfg, kv, KvCache)
     if not 1 <= n_seqs <= kv.seqs:
         raise ValueError("n_seqs is more than the caches hold")
     H, Hq, d, dev = cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim, kv.index
@@ -599,7 +600,7 @@ def attend_batch_kv(cfg: Config, Q: torch.Tensor, kv: KvCache, n_seqs: int, n_to
                     status: torch.Tensor | None = None, stream=None):
     """zha_attend_batch_kv: Q [n_seqs, Hq, d] (float32 or bf16) over the first n_tokens [n_seqs]
     (int64) tokens of each cache of kv_batch(); (out, lse), out of Q's type."""
-    _same_cache(cfg, kv)
+    _same_cache(cfg, kv, KvCache)
     if not 1 <= n_seqs <= kv.seqs:
         raise ValueError("n_seqs is more than the caches hold")
     dev, dtype = kv.index, _DTYPE.get(Q.dtype)
@@ -639,13 +640,15 @@ def page_pool(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor, refs:
 
 
 def pages_workspace_bytes(cfg: Config, pool: PagePool, n_items: int) -> int:
+    if not isinstance(pool, PagePool):
+        raise ValueError("the pool must come from page_pool()")
     return int(lib.zha_pages_workspace_bytes(byref(cfg), byref(pool), n_items))
 
 
 def pages_extend(cfg: Config, pool: PagePool, seqs: torch.Tensor, n_tokens: torch.Tensor,
                  ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_extend: pages for the first n_tokens[i] (int64) tokens of sequence seqs[i] (int32)."""
-    _same_cache(cfg, pool)
+    _same_cache(cfg, pool, PagePool)
     n, dev = seqs.numel(), pool.index
     on = _run_on(dev, stream)
     if ws is None:
@@ -660,7 +663,7 @@ def pages_extend(cfg: Config, pool: PagePool, seqs: torch.Tensor, n_tokens: torc
 def pages_fork(cfg: Config, pool: PagePool, src: torch.Tensor, dst: torch.Tensor, n_tokens: torch.Tensor,
                ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_fork: the empty sequence dst[i] becomes the first n_tokens[i] tokens of src[i]."""
-    _same_cache(cfg, pool)
+    _same_cache(cfg, pool, PagePool)
     n, dev = dst.numel(), pool.index
     on = _run_on(dev, stream)
     if ws is None:
@@ -677,7 +680,7 @@ def pages_free(cfg: Config, pool: PagePool, seqs: torch.Tensor, keep: torch.Tens
                ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_free: sequences seqs [n] give up their pages behind the first keep [n] (int64)
     tokens (None: all). Needs no workspace; ws is taken for symmetry and not used."""
-    _same_cache(cfg, pool)
+    _same_cache(cfg, pool, PagePool)
     n, dev = seqs.numel(), pool.index
     on = _run_on(dev, stream)
     st = lib.zha_pages_free(byref(cfg), byref(pool), _list_ptr(seqs, torch.int32, n, dev, "seqs"),
@@ -691,7 +694,7 @@ def pages_compact(cfg: Config, pool: PagePool, page_map: torch.Tensor | None = N
                   ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """zha_pages_compact: the pages in use become [0, n); page_map [n_pages] and n_live [1]
     (int32, both may be None) say where each went and how many they are."""
-    _same_cache(cfg, pool)
+    _same_cache(cfg, pool, PagePool)
     dev = pool.index
     on = _run_on(dev, stream)
     if ws is None:

@@ -215,3 +215,31 @@ def test_binding_refuses_what_the_c_calls_cannot_see(zha):
         zha.rope_apply(zha.Rope(64), torch.zeros(3, 2, 128), torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError):
         zha.rope_apply(zha.Rope(64), torch.zeros(3, 2, 64, dtype=torch.float64), torch.zeros(3, dtype=torch.int64))
+
+
+def _described(c, index=0):
+    """What kv_batch() and page_pool() note beside the C struct, for _cfg()'s cache."""
+    c.shape, c.dtype, c.heads, c.seqs, c.index, c.device = (500, 64, 128), 1, 4, 8, index, None
+    return c
+
+
+def test_page_calls_take_pools_and_the_others_caches(zha):
+    """A zha_kv_cache is shorter than a zha_page_pool: a page call that took one would read its
+    counts from behind it. Both are refused for each other before any pointer is taken."""
+    cfg = _cfg(zha)
+    kv = _described(_kv(zha, 500, 16))
+    pool = _described(zha.PagePool(1 << 40, 1 << 41, 500, 1 << 42, 16, 1 << 43, 8, 0))
+    assert ctypes.sizeof(kv) < ctypes.sizeof(pool)
+    ints = torch.zeros(2, dtype=torch.int32)
+    longs = torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: zha.pages_workspace_bytes(cfg, kv, 2), lambda: zha.pages_extend(cfg, kv, ints, longs),
+                 lambda: zha.pages_fork(cfg, kv, ints, ints, longs), lambda: zha.pages_free(cfg, kv, ints),
+                 lambda: zha.pages_compact(cfg, kv)):
+        with pytest.raises(ValueError, match=r"page_pool\(\)"):
+            call()
+    x = torch.zeros(2, 4, 128)
+    for call in (lambda: zha.attend_batch_kv(cfg, torch.zeros(8, 32, 128), pool, 8, longs, 10),
+                 lambda: zha.rope_append_kv(cfg, None, None, x, x, pool, 8, ints, longs)):
+        with pytest.raises(ValueError, match=r"kv_batch\(\)$"):
+            call()
+    assert zha.pages_workspace_bytes(cfg, pool, 2) > 0
