@@ -77,6 +77,12 @@ class KvCache(ctypes.Structure):
                 ("max_blocks", c_int64)]
 
 
+def _some(block_table: torch.Tensor) -> None:
+    """A table without entries has no address, and a cache without a table is a contiguous one."""
+    if block_table.numel() == 0:
+        raise ValueError("block_table must have at least one entry per sequence and KV head")
+
+
 def kv_cache(K: torch.Tensor, V: torch.Tensor | None = None,
              block_table: torch.Tensor | None = None) -> KvCache:
     """A zha_kv_cache over torch tensors: contiguous when block_table is None
@@ -89,6 +95,7 @@ def kv_cache(K: torch.Tensor, V: torch.Tensor | None = None,
     if block_table is not None:
         if not (block_table.is_cuda and block_table.dtype == torch.int32 and block_table.is_contiguous()):
             raise ValueError("block_table must be a contiguous int32 CUDA tensor [Hkv, max_blocks]")
+        _some(block_table)
         c.block_table = block_table.data_ptr()
         c.max_blocks = block_table.shape[1]
     return c
@@ -110,6 +117,7 @@ def kv_batch(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor | None 
         if not (block_table.device == K.device and block_table.dtype == torch.int32
                 and block_table.is_contiguous() and block_table.dim() == 3):
             raise ValueError("block_table must be a contiguous int32 CUDA tensor [n_seqs, Hkv, max_blocks]")
+        _some(block_table)
         c.block_table = block_table.data_ptr()
         c.max_blocks = block_table.shape[2]
     # what the calls check a configuration against (not part of the C struct)

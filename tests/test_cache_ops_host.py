@@ -243,3 +243,30 @@ def test_page_calls_take_pools_and_the_others_caches(zha):
         with pytest.raises(ValueError, match=r"kv_batch\(\)$"):
             call()
     assert zha.pages_workspace_bytes(cfg, pool, 2) > 0
+
+
+class _OnGpu:
+    """A CPU tensor that passes for one on a GPU where only a handle is made of it."""
+    is_cuda = True
+
+    def __init__(self, x):
+        self._x = x
+
+    def __getattr__(self, name):
+        return getattr(self._x, name)
+
+
+@pytest.mark.parametrize("shape", [(8, 4, 0), (0, 4, 16), (8, 0, 16)])
+def test_caches_refuse_a_block_table_without_entries(zha, shape):
+    """Its address is NULL, with which the C calls would take the pool for contiguous caches
+    of n_pages rows, and read behind it where sequences times heads are more than the chunk."""
+    pool = _OnGpu(torch.zeros(6, 64, 128, dtype=torch.bfloat16))
+    assert zha.kv_batch(pool, pool, _OnGpu(torch.zeros(8, 4, 16, dtype=torch.int32))).block_table
+    empty = torch.zeros(shape, dtype=torch.int32)
+    assert empty.data_ptr() == 0
+    with pytest.raises(ValueError, match="at least one entry"):
+        zha.kv_batch(pool, pool, _OnGpu(empty))
+    with pytest.raises(ValueError, match="at least one entry"):
+        zha.kv_cache(pool, pool, _OnGpu(empty[0] if shape[0] else torch.zeros(0, 16, dtype=torch.int32)))
+    with pytest.raises(ValueError, match="at least one entry"):
+        zha.page_pool(pool, pool, _OnGpu(empty), _OnGpu(torch.zeros(6, dtype=torch.int32)))
