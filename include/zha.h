@@ -426,8 +426,10 @@ zha_status zha_rope_append_kv(const zha_config* cfg, const zha_rope* rope, const
  * nothing between calls; calls that may overlap need one each. For finite inputs a
  * float32 result has the error of float32 sums: over a bf16 cache every operand enters
  * exactly, over a float32 cache within 2^-22; with bf16 queries weights enter within
- * 2^-16. An infinity or NaN among the inputs makes the
- * results of its own head and sequence infinite or NaN, no others. */
+ * 2^-16. An infinity or NaN in a query or key makes the output and lse of its own
+ * heads and sequence NaN, one in a value its own element of their outputs infinite or
+ * NaN, and no others. (A finite key whose score passes the range of float32
+ * downwards has a weight of 0, as in the formula.) */
 size_t zha_attend_batch_workspace_bytes(const zha_config* cfg, int32_t n_seqs, int64_t max_tokens);
 zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q_dtype,
                                const zha_kv_cache* kv, int32_t n_seqs, const int64_t* d_n_tokens,

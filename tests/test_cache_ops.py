@@ -210,6 +210,63 @@ def test_attend_values_that_are_not_finite_stay_in_their_head(zha):
     assert not torch.isfinite(out[2, 2:, 5]).any()
 
 
+@pytest.mark.parametrize("cache,q", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+def test_attend_infinite_queries_and_keys_show_in_their_heads(zha, cache, q, G):
+    """Also where every score that they reach is -inf, which a missing key's is too, and in
+    sequences that are split. The other heads and sequences are what they were, bit by bit."""
+    for lens in ([40, 40, 70], [9000, 3, 30000]):
+        b = Batch(zha, lens, 2, G, 64, 16, cache, q, seed=51)
+        b.Q[:, :, 3] = -1.0 - b.Q[:, :, 3].abs()         # so that +inf there gives -inf
+        want, wlse = b.run()
+        mine = torch.zeros_like(wlse, dtype=torch.bool)
+
+        def changed(*heads):
+            out, lse = b.run()
+            here = mine.clone()
+            for s, h in heads:
+                here[s, h] = True
+            assert out[here].isnan().all() and lse[here].isnan().all()
+            assert torch.equal(out[~here], want[~here]) and torch.equal(lse[~here], wlse[~here])
+
+        rows = [(s, h) + tuple(b.rows(s, h, n)) for s, n in enumerate(lens) for h in range(2)]
+        group = lambda s, h: [(s, h * G + i) for i in range(G)]
+        for s, h, key, e in ((0, 1, lens[0] - 1, math.inf), (2, 0, 17, math.inf), (2, 0, 17, -math.inf), (0, 0, 0, math.nan)):
+            page, at = (x[key] for x in rows[2 * s + h][2:])
+            kept = b.K[page, at, 3].clone()
+            b.K[page, at, 3] = e
+            changed(*group(s, h))
+            b.K[page, at, 3] = kept
+        # all scores of a query -inf: the keys' element has one sign
+        for s, h, page, at in rows:
+            b.K[page, at, 5] = 1.0 + b.K[page, at, 5].abs()
+        want, wlse = b.run()
+        for s, h, e in ((2, 2 * G - 1, -math.inf), (0, 0, math.inf), (1, G // 2, math.nan)):
+            kept = b.Q[s, h, 5].clone()
+            b.Q[s, h, 5] = e
+            changed((s, h))
+            b.Q[s, h, 5] = kept
+        # a sequence without a page in the pool has no keys, whatever its query
+        b.Q[0, 0, 5] = -math.inf
+        b.table[0] = -1
+        out, lse = b.run()
+        assert (out[0] == 0).all() and (lse[0] == -math.inf).all()
+
+
+@pytest.mark.parametrize("cache,q", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+def test_attend_finite_scores_below_the_range_weigh_nothing(zha, cache, q, G):
+    """-1e60 and -1e34 are weights of 0 both, though only the second is a float32."""
+    b = Batch(zha, [40, 5], 1, G, 64, 16, cache, q, paged=False, seed=52)
+    b.K[..., 3] = 0.0
+    b.Q[..., 3] = 1e30
+    b.K[0, 0, 7, 3] = -1e4
+    want, wlse = b.run()
+    b.K[0, 0, 7, 3] = -1e30
+    out, lse = b.run()
+    assert torch.isfinite(want).all() and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_attend_bad_lengths_are_clamped(zha):
     b = Batch(zha, [50, 60, 70], 2, 4, 64, 16, BF, F32, seed=8)
     for lens in ([50, -3, 70], [50, 60, 1 << 40]):
