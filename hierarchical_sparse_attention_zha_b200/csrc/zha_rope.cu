@@ -508,7 +508,7 @@ zha_status zha_rope_init(const zha_rope_spec* c, zha_rope* out) {
       return D * std::log(c->original_tokens / (two_pi * turns)) / (2.0 * std::log(c->base));
     };
     lo = std::fmax(0.0, std::floor(where(c->high)));
-    hi = std::fmin(double(c->pairs - 1), std::ceil(where(c->low)));
+    hi = std::fmin(double(D - 1), std::ceil(where(c->low)));
   }
   zha_rope r{};
   r.head_dim = c->head_dim;

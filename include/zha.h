@@ -340,7 +340,7 @@ typedef enum {
     ZHA_ROPE_LINEAR = 1, /* theta_i / factor: positions interpolated */
     ZHA_ROPE_NTK = 2,    /* base * factor^(freq_dim / (freq_dim - 2)); freq_dim 2: as LINEAR */
     ZHA_ROPE_YARN = 3,   /* theta_i (1 - w) + theta_i / factor * w, w = clamp((i - lo) / max(hi - lo, 0.001)) to
-                            [0, 1], lo = max(0, floor(x(high))), hi = min(pairs - 1, ceil(x(low))), x(n) = freq_dim
+                            [0, 1], lo = max(0, floor(x(high))), hi = min(freq_dim - 1, ceil(x(low))), x(n) = freq_dim
                             ln(original_tokens / (2 pi n)) / (2 ln base): the pairs that turn more than `high`
                             times over the original length stay, those below `low` turns are
                             interpolated. amplitude 0 stands for 0.1 ln(factor) + 1 */

@@ -27,6 +27,23 @@ def pytest_configure(config):
         build.build()
 
 
+# Cases that hold a wrong value, with the proof. They run, and are expected to fail.
+_WRONG_VALUES = {
+    "test_cache_ops_host.py::test_rope_table_holds_the_formulas_frequencies[64-13-64-1000000.0-yarn]":
+        "its formula cuts YaRN's ramp to the pairs that turn; the method cuts it to freq_dim - 1. Here x(32) = "
+        "64 ln(4096 / 64 pi) / (2 ln 1e6) = 6.98 and x(1) = 15.01, so the ramp is 6..16 and pair 12 is 6 / 10 "
+        "interpolated, not wholly: it turns 4096 * 1e6^(-24 / 64) / 2 pi = 3.7 times over the original length, "
+        "more than low = 1. test_yarn_ramp_ends_where_the_method_ends_it has such cases worked out.",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        for case, why in _WRONG_VALUES.items():
+            if item.nodeid.endswith(case):
+                item.add_marker(pytest.mark.xfail(reason=why, strict=True))
+
+
 @pytest.fixture(scope="session")
 def golden_dir():
     return os.path.join(ROOT, "tests", "golden")

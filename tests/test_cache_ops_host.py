@@ -270,3 +270,29 @@ def test_caches_refuse_a_block_table_without_entries(zha, shape):
         zha.kv_cache(pool, pool, _OnGpu(empty[0] if shape[0] else torch.zeros(0, 16, dtype=torch.int32)))
     with pytest.raises(ValueError, match="at least one entry"):
         zha.page_pool(pool, pool, _OnGpu(empty), _OnGpu(torch.zeros(6, dtype=torch.int32)))
+
+
+@pytest.mark.parametrize("args,kept", [
+    # x(32) = 128 ln(4096 / 64 pi) / (2 ln 10000) = 20.9 and x(1) = 45.03: the ramp is 20..46, beyond
+    # the 32 pairs that turn; pair 31 turns 7.5 times over the original length
+    (dict(head_dim=128, pairs=32, freq_dim=128, factor=8.0, original_tokens=4096.0, high=32.0),
+     {0: 0, 20: 0, 21: 1 / 26, 30: 10 / 26, 31: 11 / 26}),
+    # x(32) = 45.03, x(1) = 69.1: 45..70
+    (dict(head_dim=128, pairs=64, factor=4.0, original_tokens=131072.0, high=32.0),
+     {45: 0, 46: 1 / 25, 62: 17 / 25, 63: 18 / 25}),
+    # x(32) = 2.87, x(1) = 5.12: 2..6
+    (dict(head_dim=64, pairs=6, factor=8.0, original_tokens=16384.0, high=32.0),
+     {1: 0, 2: 0, 3: 1 / 4, 4: 2 / 4, 5: 3 / 4}),
+    # x(10000) = 8 ln(100 / 2 pi) / (2 ln 100) = 2.4, x(1) = 10.4: cut to freq_dim - 1 = 7, 2..7
+    (dict(head_dim=64, pairs=4, base=100.0, factor=8.0, original_tokens=1e6, high=10000.0), {2: 0, 3: 1 / 5}),
+    # a ramp inside the pairs: x(32) = 20.9, x(1) = 45.03 of 64
+    (dict(head_dim=128, pairs=64, factor=8.0, original_tokens=4096.0, high=32.0), {20: 0, 33: 13 / 26, 46: 1, 63: 1}),
+])
+def test_yarn_ramp_ends_where_the_method_ends_it(zha, args, kept):
+    """The published ramp runs from floor(x(high)) to ceil(x(low)), cut to [0, freq_dim - 1] and
+    not to the pairs that there are. `kept`: pair -> its interpolated part, worked out by hand."""
+    base, f, D = args.get("base", 10000.0), args["factor"], args.get("freq_dim") or 2 * args["pairs"]
+    r = zha.Rope(layout="half", scaling="yarn", low=1.0, **args).table
+    for i, w in kept.items():
+        want = base ** (-2.0 * i / D) * ((1 - w) + w / f) / (2 * math.pi)
+        assert abs(r.turn[i] / 2.0 ** 64 - want) <= 2.0 ** -46 * want, i
