@@ -87,6 +87,17 @@ def _rope_args(c):
     return a
 
 
+def _own_rope(c):
+    """The case's rotation as the library is asked for it. The forms in this file end a yarn ramp at
+    the last pair at the latest, the library at freq_dim - 1 = 2 pairs - 1. Where x(low) lies beyond the
+    last pair (6 pairs or fewer here), a `low` whose x is just below it asks for the same ramp."""
+    a = _rope_args(c)
+    if c["scaling"] == "yarn" and c["pairs"] > 1:
+        last = a["original_tokens"] / (2 * math.pi) * a["base"] ** (-(c["pairs"] - 1.02) / c["pairs"])
+        a["low"] = max(a["low"], last)
+    return _lib().Rope(**a)
+
+
 # ---------------------------------------------------------------------------
 # Inputs
 # ---------------------------------------------------------------------------
@@ -181,14 +192,14 @@ def prepare(case, seed):
         if own:
             zha = _lib()
             s["cfg"] = _config(c, hq)
-            s["rope"] = zha.Rope(**_rope_args(c))
+            s["rope"] = _own_rope(c)
             s["kvc"] = zha.kv_batch(s["K"], s["V"], s["table"])
             s["out"] = torch.empty(T, hq, d, dtype=DTYPES[c["q"]], device="cuda")
     elif c["op"] == "apply":
         s["X"] = _randn(g, (c["new"], c["heads"], c["d"]), DTYPES[c["src"]])
         s["pos"] = torch.from_numpy(r.integers(0, c["far"] + 1, c["new"])).cuda()
         if own:
-            s["rope"] = _lib().Rope(**_rope_args(c))
+            s["rope"] = _own_rope(c)
             s["out"] = torch.empty(c["new"], c["heads"], c["d"], dtype=DTYPES[c["out"]], device="cuda")
     else:
         s.update(_pages_state(c, r, g))
