@@ -442,10 +442,10 @@ zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q
  * the table entries that name page p, 0 = free. The calls run on the device alone
  * (capturable) and always hand out the lowest free pages, in the order item, KV head,
  * block, so that a run can be repeated exactly. Lists are int32 [n_items] sequence
- * indexes with int64 token counts. An item whose index is out of range or
- * already listed is refused (ZHA_DEV_BAD_SEQUENCE), one whose count does not fit in
- * max_blocks pages too (ZHA_DEV_BAD_LENGTH); the others go ahead. n_items = 0 does
- * nothing. Calls on one pool need an order (a stream) between them. */
+ * indexes with int64 token counts. An item of extend or fork whose index is out of
+ * range or already listed is refused (ZHA_DEV_BAD_SEQUENCE), one whose count is negative or
+ * does not fit in max_blocks pages too (ZHA_DEV_BAD_LENGTH); the others go ahead. Free
+ * says below what it refuses. n_items = 0 does nothing. Calls on one pool need an order (a stream) between them. */
 typedef struct {
     void* k;                /* K pool [n_pages][C][head_dim] */
     void* v;                /* V pool, the same shape */
@@ -482,7 +482,8 @@ zha_status zha_pages_fork(const zha_config* cfg, const zha_page_pool* pool, cons
 
 /* Give up the blocks from ceil(d_keep[i] / C) on (d_keep NULL: all blocks) of
  * sequence d_seqs[i]: refs - 1, entry -1; a page at 0 is free. A sequence listed twice
- * keeps the smaller count. An entry that names no page in use is cleared
+ * keeps the smaller count, and one whose count is more than max_blocks pages hold
+ * keeps all that it has; a negative count is refused (ZHA_DEV_BAD_LENGTH). An entry that names no page in use is cleared
  * (ZHA_DEV_BAD_PAGE). Cut back inside a shared page, a sequence must not be
  * written there: fork it first. */
 zha_status zha_pages_free(const zha_config* cfg, const zha_page_pool* pool, const int32_t* d_seqs,

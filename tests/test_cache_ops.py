@@ -891,6 +891,24 @@ def test_pages_all_or_nothing_refusals_and_edges(zha):
     assert p.free([3]) == z.ZHA_DEV_BAD_PAGE
 
 
+def test_pages_free_with_counts_beyond_the_table_keeps_everything(zha):
+    """Nothing lies behind them. Extend and fork, which would need pages there, refuse such a
+    count, and all of them a negative one."""
+    p = Pages(zha, 4, 2, 4, 4, 20)
+    assert p.extend([0, 1], [16, 5]) == 0
+    table, refs = p.t.copy(), p.r.copy()
+    for keep in (16, 17, 1 << 33, (1 << 63) - 1):
+        assert p.free([0, 1], [keep, keep]) == 0
+        assert np.array_equal(p.t, table) and np.array_equal(p.r, refs)
+        if keep > 16:
+            assert p.extend([0], [keep]) == zha.ZHA_DEV_BAD_LENGTH
+            assert p.fork([0], [2], [keep]) == zha.ZHA_DEV_BAD_LENGTH
+    for n in (-1, -(1 << 63)):
+        assert p.free([0], [n]) == p.extend([0], [n]) == p.fork([0], [2], [n]) == zha.ZHA_DEV_BAD_LENGTH
+    assert p.free([1, 0, 1], [1 << 40, 4, 4]) == 0                                # twice: the smaller count
+    assert p.t[1].tolist() == [[8, -1, -1, -1], [10, -1, -1, -1]]
+
+
 def test_pages_long_lists(zha):
     """More items than a CTA keeps of a list, and more rows than it keeps offsets of."""
     rng = np.random.default_rng(7)
