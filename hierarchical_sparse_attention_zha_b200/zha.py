@@ -110,6 +110,8 @@ def kv_batch(K: torch.Tensor, V: torch.Tensor, block_table: torch.Tensor | None 
             raise ValueError("caches must be contiguous CUDA tensors [n_seqs, Hkv, ld, d], or pools [n_pages, C, d]")
     if K.shape != V.shape or K.dtype != V.dtype or K.device != V.device:
         raise ValueError("K and V must have one shape, type and device")
+    if K.dtype not in _DTYPE:
+        raise ValueError("K and V must be float32 or bfloat16")
     c = KvCache()
     c.k, c.v = K.data_ptr(), V.data_ptr()
     c.ld = K.shape[2] if block_table is None else K.shape[0]

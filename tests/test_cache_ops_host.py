@@ -296,3 +296,16 @@ def test_yarn_ramp_ends_where_the_method_ends_it(zha, args, kept):
     for i, w in kept.items():
         want = base ** (-2.0 * i / D) * ((1 - w) + w / f) / (2 * math.pi)
         assert abs(r.turn[i] / 2.0 ** 64 - want) <= 2.0 ** -46 * want, i
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int8])
+def test_caches_refuse_other_element_types(zha, dtype):
+    """With the ValueError of the other checks."""
+    x = _OnGpu(torch.zeros(6, 64, 128, dtype=dtype))
+    table = _OnGpu(torch.zeros(8, 4, 16, dtype=torch.int32))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        zha.kv_batch(x, x, table)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        zha.page_pool(x, x, table, _OnGpu(torch.zeros(6, dtype=torch.int32)))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        zha.kv_batch(_OnGpu(torch.zeros(2, 4, 9, 128, dtype=dtype)), _OnGpu(torch.zeros(2, 4, 9, 128, dtype=dtype)))
