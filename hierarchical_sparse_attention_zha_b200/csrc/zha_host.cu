@@ -2,7 +2,6 @@
 // zha_host.cuh). Every entry is written once under a mutex and read afterwards.
 #include <mutex>
 #include <unordered_map>
-#include <unordered_set>
 
 #include "zha_host.cuh"
 
@@ -14,7 +13,7 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices] = {};
 std::unordered_map<const void*, size_t> g_smem[kMaxDevices];
-std::unordered_set<const void*> g_wide[kMaxDevices];
+std::unordered_map<const void*, int> g_wide[kMaxDevices];
 
 }  // namespace
 
@@ -74,16 +73,33 @@ cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
   return cudaSuccess;
 }
 
-cudaError_t ensure_wide_cluster(const void* kernel) {
+cudaError_t widest_cluster(const void* kernel, int threads, int* ctas) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices)
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const bool kept = dev >= 0 && dev < kMaxDevices;
   std::lock_guard<std::mutex> lock(g_mutex);
-  if (g_wide[dev].count(kernel)) return cudaSuccess;
+  if (kept) {
+    const auto it = g_wide[dev].find(kernel);
+    if (it != g_wide[dev].end()) { *ctas = it->second; return cudaSuccess; }
+  }
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-  g_wide[dev].insert(kernel);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(unsigned(threads));
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int fit = 0;
+  if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();                    // a size that the device does not know
+    fit = 0;
+  }
+  *ctas = fit > 0 ? 16 : 8;
+  if (kept) g_wide[dev][kernel] = *ctas;
   return cudaSuccess;
 }
 

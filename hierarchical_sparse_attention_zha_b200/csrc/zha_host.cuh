@@ -28,7 +28,8 @@ inline cudaError_t ensure_dynamic_smem(void (*kernel)(Args...), size_t bytes) {
   return ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes);
 }
 
-// Clusters of more than 8 CTAs for `kernel` on the current device.
-cudaError_t ensure_wide_cluster(const void* kernel);
+// The CTAs of the widest cluster of `kernel`, with `threads` each, that the current device can
+// hold: 16, where a GPC has the SMs free for them, or the portable 8.
+cudaError_t widest_cluster(const void* kernel, int threads, int* ctas);
 
 }  // namespace zha

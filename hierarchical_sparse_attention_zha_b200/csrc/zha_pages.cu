@@ -541,15 +541,26 @@ zha_status launch_page_kernel(const char* name, const char* who, void (*kernel)(
   return e == cudaSuccess ? ZHA_OK : zha_report_cuda(e, who);
 }
 
-// One cluster, of one CTA per 4096 counts or 32 rows.
+// One cluster, of one CTA per 4096 counts or 32 rows: a power of two, up to the `most`
+// that the device can hold. The kernels take any number.
+constexpr int book_ctas(int64_t n_pages, int64_t rows, int most) {
+  const int64_t by_pages = (n_pages + 4095) / 4096, by_rows = (rows + 31) / 32;
+  int ctas = 1;
+  while (ctas < (by_pages > by_rows ? by_pages : by_rows) && ctas < most) ctas *= 2;
+  return ctas;
+}
+static_assert(book_ctas(1, 0, 16) == 1 && book_ctas(4097, 0, 16) == 2 && book_ctas(1, 160, 16) == 8 &&
+                  book_ctas(65536, 0, 16) == 16 && book_ctas(int64_t(1) << 30, 1 << 24, 16) == kMostCtas &&
+                  book_ctas(65536, 0, 8) == 8 && book_ctas(int64_t(1) << 30, 1 << 24, 8) == 8,
+              "no more CTAs than fit, and none without work");
+
 template <typename... K, typename... A>
 zha_status launch_book(const char* name, const char* who, void (*kernel)(K...), const PoolArgs& P, int64_t rows,
                        cudaStream_t s, A&&... args) {
-  const int64_t want = max64((P.n_pages + 4095) / 4096, (rows + 31) / 32);
-  int ctas = 1;
-  while (ctas < want && ctas < kMostCtas) ctas *= 2;
-  cudaError_t e = ensure_wide_cluster(reinterpret_cast<const void*>(kernel));
+  int most = 0;
+  cudaError_t e = widest_cluster(reinterpret_cast<const void*>(kernel), kBookThreads, &most);
   if (e != cudaSuccess) return zha_report_cuda(e, who);
+  const int ctas = book_ctas(P.n_pages, rows, most);
   TraceScope ts(name, 0, s);
   zha_count_launch();
   cudaLaunchConfig_t cfg = {};

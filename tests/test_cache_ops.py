@@ -981,6 +981,53 @@ def test_pages_captured_with_one_workspace(zha):
         zha.pages_extend(p.cfg, p.pool, every, new, ws=ws[:64])
 
 
+def test_first_calls_of_a_process_may_be_captured():
+    """What a call finds out about the device once (shared memory, the cluster that fits) is no
+    work of a stream: a graph of calls that never ran before gives the results of direct calls."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from hierarchical_sparse_attention_zha_b200 import zha
+cfg = zha.make_config(2, 8, 64, 16, 1, 1, torch.bfloat16, 4096)
+K = torch.randn(70000, 16, 64, device="cuda").bfloat16()
+V = torch.randn_like(K)
+def state():
+    table = torch.full((40, 2, 4), -1, dtype=torch.int32, device="cuda")
+    refs = (torch.arange(70000, device="cuda") % 3 == 0).int()
+    return table, refs, K.clone(), V.clone()
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+i64 = lambda v: torch.tensor(v, device="cuda")
+a, b, n, n2, many = i32(range(20)), i32(range(20, 40)), i64([33] * 20), i64([40] * 40), i32(range(40))
+x, seq, at, rope = torch.randn(40, 12, 64, device="cuda"), i32(range(40)), i64([39] * 40), zha.Rope(64)
+def step(t, r, k, v, out):
+    pool, kv = zha.page_pool(k, v, t, r), zha.kv_batch(k, v, t)
+    zha.pages_extend(cfg, pool, a, n)
+    zha.pages_fork(cfg, pool, a, b, n)
+    zha.pages_extend(cfg, pool, many, n2)
+    q = zha.rope_append_kv(cfg, rope, x[:, :8], x[:, 8:10], x[:, 10:], kv, 40, seq, at)
+    zha.pages_compact(cfg, pool)
+    zha.attend_batch_kv(cfg, q, kv, 40, n2, 40, out=out)
+    zha.pages_free(cfg, pool, b)
+one, two = state(), state()
+o1, o2 = torch.empty(40, 8, 64, device="cuda"), torch.empty(40, 8, 64, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step(*one, o1)
+g.replay()
+step(*two, o2)
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip((*one, o1), (*two, o2)))
+assert (one[0][:20, :, :3] >= 0).all() and (one[0][20:] == -1).all()
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_append_and_pages_at_the_end_of_a_large_pool(zha):
     """Rows beyond 2^32 bytes and 2^31 elements: 300,000 pages of 64 rows of 128 bf16."""
     pages, C, d = 300000, 64, 128
