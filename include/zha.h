@@ -329,7 +329,10 @@ zha_status zha_sparse_attend_kv(const zha_tree* tree, const float* d_Q, const zh
  * Pair i of a head is turned by pos * theta_i: (a, b) -> A (a cos - b sin, a sin +
  * b cos), with theta_i = base^(-2i / freq_dim). The elements behind the pairs
  * stay as they are. Angles are kept as 64-bit fractions of a turn, so that a
- * far position loses nothing. */
+ * far position loses nothing. A tree with positions (zha_config's rope_pairs) reads keys
+ * of one rotation only: INTERLEAVED, PLAIN, pairs = rope_pairs, freq_dim = head_dim, base =
+ * rope_base, amplitude 1. Keys turned in any other way are for dense attention, or
+ * for a tree with rope_pairs = 0, which takes the cache's keys as they are. */
 typedef enum {
     ZHA_ROPE_INTERLEAVED = 0, /* pair i = elements (2i, 2i + 1), the tree's layout (rope_pairs) */
     ZHA_ROPE_HALF = 1         /* pair i = elements (i, i + pairs) */

@@ -683,6 +683,69 @@ def test_append_padding_and_bad_targets_write_nothing(zha):
         assert torch.equal(c["vc"][keep[s, 1, at // 16].long(), at % 16], c["V"][t, 1])
 
 
+@pytest.mark.parametrize("d,pairs,base,paged", [(64, 8, 10000.0, True), (64, 32, 500.0, False), (128, 48, 10000.0, True)])
+def test_a_tree_with_positions_reads_keys_that_append_turned(zha, d, pairs, base, paged):
+    """freq_dim = head_dim in the interleaved layout is the tree's rope_pairs. Raw keys written by
+    zha_rope_append_kv, summarised by a tree with positions, against the oracle's tree of the
+    raw keys turned in 64 bits: every element of every level, to the summaries' tolerance
+    (the keys' own error, 8 * 2^-24, is far below). Keys turned the other way, in the other layout
+    or with freq_dim = 2 * pairs are seen: in the oracle they are off by 100 times as much."""
+    import oracle as O
+    from _parity import SUMMARY_RTOL, summary_errors
+
+    H, C, L, R, T = 2, 16, 2, 4, 16 * 16 * 2
+    cfg = zha.make_config(H, 4, d, C, L, R, F32, T, rope_pairs=pairs, rope_base=base)
+    g = _gen(60)
+    raw = torch.randn(T, H, d, device="cuda", generator=g)
+    V = torch.randn(T, H, d, device="cuda", generator=g)
+    q = torch.randn(T, 4, d, device="cuda", generator=g)
+    refq = torch.randn(H, R, d, device="cuda", generator=g)
+    blocks = T // C
+    table = torch.randperm(H * blocks, device="cuda", generator=g).to(torch.int32).reshape(1, H, blocks) if paged else None
+    kc = torch.zeros((H * blocks, C, d) if paged else (1, H, T, d), device="cuda")
+    vc = torch.zeros_like(kc)
+    at = torch.arange(T, device="cuda")
+    turned_q = zha.rope_append_kv(cfg, zha.Rope(d, pairs, "interleaved", base, freq_dim=d), q, raw, V,
+                                  zha.kv_batch(kc, vc, table), 1, torch.zeros(T, dtype=torch.int32, device="cuda"), at)
+    tree = zha.Tree(cfg, refq)
+    one = zha.kv_cache(kc if paged else kc[0], vc if paged else vc[0], table[0] if paged else None)
+    tree.build_kv(one, T)
+    pos = np.arange(T)
+    wrong = [dict(pos=-pos), dict(freq=2 * pairs), dict(half=True)]
+
+    def keys64(x, pos=pos, freq=d, half=False):
+        i = np.arange(pairs)
+        z = np.exp(1j * pos[:, None] * base ** (-2.0 * i / freq))
+        y, (u, v) = x.copy(), ((slice(0, pairs), slice(pairs, 2 * pairs)) if half else
+                               (slice(0, 2 * pairs, 2), slice(1, 2 * pairs, 2)))
+        w = z * (x[:, u] + 1j * x[:, v])
+        y[:, u], y[:, v] = w.real, w.imag
+        return y
+
+    for h in range(H):
+        x, r = raw[:, h].double().cpu().numpy(), refq[h].double().cpu().numpy()
+        build = lambda **kw: O.build_tree_rope(keys64(x, **kw), r, C, L, T, base, pairs)
+        want, others = build(), [build(**kw) for kw in wrong if kw.get("freq") != d]
+        for lvl in (1, 2):
+            n = want.n_nodes(lvl)
+            kh, bh = (y[h, :n].double().cpu().numpy() for y in tree.level(lvl))
+            ek, eb = summary_errors(kh, bh, *want.nodes[lvl])
+            assert ek <= SUMMARY_RTOL and eb <= SUMMARY_RTOL, (lvl, ek, eb)
+            for other in others:
+                assert summary_errors(*other.nodes[lvl], *want.nodes[lvl])[0] > 100 * SUMMARY_RTOL
+    # and the queries turned with them: all chunks kept, the last token's attention
+    ids, cnt = tree.route(turned_q[-1:], T, 1.0, T // C)
+    out, lse = tree.sparse_attend_kv(turned_q[-1:], one, T, ids, cnt)
+    assert (cnt == T // C).all()
+    for j in range(4):
+        h = j // 2
+        w = keys64(raw[:, h].double().cpu().numpy()) @ keys64(q[-1:, j].double().cpu().numpy(), pos[-1:])[0] / math.sqrt(d)
+        p = np.exp(w - w.max())
+        o = p @ V[:, h].double().cpu().numpy() / p.sum()
+        assert np.abs(out[0, j].double().cpu().numpy() - o).max() <= 2e-5 * float(V[:, h].abs().max()) + 2e-6
+        assert abs(float(lse[0, j]) - (w.max() + np.log(p.sum()))) <= 2e-5 * max(1.0, abs(w.max() + np.log(p.sum())))
+
+
 # ---------------------------------------------------------------------------
 # Pages
 # ---------------------------------------------------------------------------
