@@ -190,6 +190,115 @@ def test_attend_keeps_the_low_bits_of_queries_and_weights(zha):
         b.check(*b.run())
 
 
+@pytest.mark.parametrize("cache,d,n", [(BF, 128, 16), (BF, 64, 32), (BF, 128, 23), (F32, 128, 16), (F32, 64, 40)])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+def test_attend_weights_enter_with_all_their_bits(zha, cache, d, n, G):
+    """Values of 1: the output is the sum of the weights that entered over their fp32 sum, and
+    must be 1. With fp32 queries over bf16 a weight is three bf16 terms, exact; cut to two it lacks 1.0e-5
+    of itself on average (2^-17 of a value in [1/2, 1)), all of one sign. Over fp32 it is two rounded
+    tf32 terms (2^-23). What else is rounded, in units of 2^-24: T tiles of three instructions,
+    two additions of 2^-23 each (relative to the tile: 12), two roundings a tile of the running
+    sum and its scaling, the same of the fp32 sum with n / 8 + 3 additions in lanes, 9 and 8 where
+    warps join, and the final quotient 3."""
+    b = Batch(zha, [n], 1, G, d, 64, cache, F32, seed=70 + G)
+    b.Q *= 0.25                                              # weights of one magnitude
+    b.V[b.rows(0, 0, n)] = 1.0
+    b.kv = zha.kv_batch(b.K, b.V, b.table)
+    T = -(-n * d * (2 if cache == BF else 4) // 4096)
+    tol = (12 + 2 * T + 9 + n / 8 + 3 + 8 + 2 * T + 3) * 2.0 ** -24 + (2.0 ** -23 if cache == F32 else 0)
+    out, _ = b.run()
+    assert ((out.double() - 1).abs() <= tol).all(), (out.double() - 1).abs().max() / tol
+    # the test sees two terms: the weights of these queries, cut to 16 bits
+    w = b.Q[0].double() @ b.K[b.rows(0, 0, n)].double().T / math.sqrt(d)
+    w = torch.exp(w - w.amax(1, keepdim=True)).float()
+    cut = lambda x: (x.view(torch.int32) & -65536).view(torch.float32)
+    two = cut(w).double() + cut(w - cut(w)).double()
+    assert cache == F32 or ((1 - two.sum(1) / w.double().sum(1)) > 1.5 * tol).float().mean() > 0.9
+
+
+@pytest.mark.parametrize("cache,q,H,G,C,lens", [
+    (BF, F32, 1, 8, 64, [200003, 0, 5, 66667]), (F32, F32, 1, 4, 64, [100001, 7]), (BF, F32, 2, 16, 16, [120000, 31000]),
+    (BF, BF, 1, 9, 64, [230000, 0, 3, 180001, 60000]), (BF, F32, 2, 4, 16, [(i * 1009) % 24000 for i in range(45)])])
+def test_attend_long_outputs_to_their_last_piece(zha, cache, q, H, G, C, lens):
+    """Outputs of long sequences are small sums of many values, so an element's bound is counted in
+    its own sum of magnitudes A = sum w |v|, not in the largest value. Of it: twice (numerator and
+    denominator) the weights' error, 2 ex + 2^-21 + their terms, with a score's error ex as in check();
+    and twice the roundings of 2^-24 on one value's way: 12 in its tile, two for each of the at most T
+    tiles that a warp has of the unit, two for each of at most 3 CTAs an SM. The test sees what it is
+    for: outputs of 0, and a 16th of the keys left out, pass it nowhere near."""
+    b = Batch(zha, lens, H, G, 128, C, cache, q, seed=71)
+    out, lse = b.run()
+    b.check(out, lse)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = sum(-(-n * 128 * (2 if cache == BF else 4) // 4096) + 2 for n in lens) * H
+    T = max(9, tiles / (8 * sms) + 1)
+    seen = [0, 0, 0]
+    for s, n in enumerate(lens):
+        for h in range(H if n else 0):
+            heads = slice(h * G, (h + 1) * G)
+            Q = b.Q[s, heads].double()
+            K, V = (x[b.rows(s, h, n)].double() for x in (b.K, b.V))
+            w = torch.softmax(Q @ K.T / math.sqrt(128), 1)
+            o, A = w @ V, w @ V.abs()
+            ex = (128 / 8 + 9) * 2.0 ** -23 * (Q.abs() @ K.abs().T).amax(1, keepdim=True) / math.sqrt(128)
+            terms = 2.0 ** -16 if q == BF else 2.0 ** -22
+            tol = A * (2 * (2 * ex + 2.0 ** -21 + terms) + (12 + 2 * T + 6 * sms) * 2.0 ** -23)
+            tol = tol + (2.0 ** -8 * (o.abs() + tol) if q == BF else 0)
+            off = (out[s, heads].double() - o).abs()
+            assert (off <= tol).all(), (off / tol).max()
+            if n > 20000:
+                lost = slice(n // 2, n // 2 + n // 16)
+                gone = (w[:, lost] @ V[lost]).abs()
+                seen = [seen[0] + o.numel(), seen[1] + (o.abs() > 4 * tol).sum(), seen[2] + (gone > 4 * tol).sum()]
+    # of zero-mean outputs a few are near 0: |o| > 4 tol for at least 3 of 4
+    assert seen[1] >= 0.75 * seen[0] and seen[2] >= (0.5 if q == BF else 0.75) * seen[0], seen
+
+
+@pytest.mark.parametrize("cache,G,ld", [(BF, 8, 1 << 21), (BF, 3, 1 << 21), (F32, 8, 1 << 20)])
+def test_attend_sums_long_sequences_by_rounded_additions(zha, cache, G, ld):
+    """The matrix instructions cut their sums off, which over the tiles of a long sequence adds up;
+    tiles are summed by rounded additions, whose errors cancel. Weights of exactly 1 (queries of 0)
+    and positive values of many magnitudes (e^-10 to 1): o is their mean. Relative to it:
+      - in a tile 16 products, each cut at 2^-24 of the largest at worst (fp32: 8 in each of three
+        instructions, and 2^-22 of a value's two terms);
+      - the tiles of a warp (some 400): independent errors of at most 2^-24 of the running sum, in
+        1,184 warps and more; their sum's standard deviation is below 2^-26, six of them 2^-23.5;
+      - 3 additions of a CTA's warps, one product and one quotient: 5 * 2^-24;
+      - the join: in each of 8 warps 14 or 19 pieces one after the other, then 8 parts. Each error is at
+        most 2^-24 of what is summed so far, the squares of which add up to below 4 of the whole's;
+        by Hoeffding's bound their sum passes 2^-24 sqrt(2 * 4 ln(2 / p)) with a probability of p:
+        14 * 2^-24 for p = 10^-10.
+    Cut additions over the 400 tiles are off by some 400 * 0.18 * 2^-23 = 9e-6: the test adds them up
+    so, too, and finds that beyond twice the bound."""
+    H, d = 4, 128
+    K = torch.zeros(1, H, ld, d, dtype=cache, device="cuda")
+    V = torch.empty_like(K)
+    g = _gen(72)
+    for h in range(H):
+        V[0, h] = torch.exp(-10 * torch.rand(ld, d, device="cuda", generator=g)).to(cache)
+    cfg = _cfg(zha, H, G, d, 64, cache)
+    n = ld - 5
+    out, lse = zha.attend_batch_kv(cfg, torch.zeros(1, H * G, d, device="cuda"), zha.kv_batch(K, V), 1,
+                                   torch.tensor([n], device="cuda"), n)
+    tol = ((16 if cache == BF else 24 + 4) + 2 ** 0.5 + 5 + 14) * 2.0 ** -24
+    keys = 16 if cache == BF else 8
+    warps = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    for h in range(H):
+        want = sum(V[0, h, i:min(n, i + (1 << 18))].double().sum(0) for i in range(0, n, 1 << 18)) / n
+        off = (out[0, h * G:(h + 1) * G].double() / want - 1).abs().max()
+        assert off <= tol, off / tol
+    assert (lse - math.log(n)).abs().max() <= 2.0 ** -22 * math.log(n)
+    # one head's tiles dealt to its share of the warps, summed with additions that are cut
+    per = n // keys // (warps // H)
+    T = V[0, 0, : per * (warps // H) * keys, :8].double().reshape(warps // H, per, keys, 8).sum(2)
+    o = torch.zeros(warps // H, 8, dtype=torch.float64, device="cuda")
+    for i in range(per):
+        exact = o + T[:, i].float().double()
+        near = exact.float()
+        o = torch.where(near.double() > exact, torch.nextafter(near, torch.zeros_like(near)), near).double()
+    assert (1 - o.sum(0) / T.sum((0, 1))).min() > 2 * tol
+
+
 def test_attend_large_scores_and_equal_scores(zha):
     b = Batch(zha, [300, 77], 1, 8, 64, 16, BF, F32, seed=6, scale=30.0)
     b.check(*b.run())
