@@ -419,8 +419,8 @@ zha_status zha_rope_append_kv(const zha_config* cfg, const zha_rope* rope, const
  * sqrt(d)) v_j with n = d_n_tokens[s] (int64, in device memory), query head h on KV head
  * h / (n_q_heads / n_kv_heads). The dense arm of the decode step, for short
  * contexts, which routing does not pay for, and to measure routing against. d_Q and
- * d_O [n_seqs][n_q_heads][head_dim] have type q_dtype (float32 or bf16), d_lse
- * (nullable) float32 [n_seqs][n_q_heads]. n = 0, or no page of the sequence
+ * d_O [n_seqs][n_q_heads][head_dim] have type q_dtype (float32 or bf16) and may be one
+ * buffer, but must not overlap otherwise; d_lse (nullable) float32 [n_seqs][n_q_heads]. n = 0, or no page of the sequence
  * in the pool: o = 0, lse = -inf. A count outside [0, max_tokens] is clamped
  * (ZHA_DEV_BAD_LENGTH). Keys whose table entry is outside the pool count as
  * absent (ZHA_DEV_BAD_PAGE). Rows behind n are not read. Requires max_tokens <= ld, or

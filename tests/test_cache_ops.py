@@ -485,6 +485,17 @@ def test_attend_without_lse_or_status(zha, lens):
     assert rc == zha.ZHA_OK and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("q", [BF, F32])
+@pytest.mark.parametrize("lens", [[300, 0, 17], [90000, 0, 17, 4000], [(i * 37) % 400 for i in range(300)]])
+def test_attend_writes_over_its_queries(zha, q, lens):
+    b = Batch(zha, lens, 2, 9, 64, 16, BF, q, seed=22)
+    want, wlse = b.run()
+    for _ in range(3):
+        b2 = b.Q.clone()
+        out, lse = zha.attend_batch_kv(b.cfg, b2, b.kv, b.S, b.n, b.most, out=b2)
+        assert out is b2 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_attend_two_calls_at_once(zha):
     """Two streams, a workspace each, over one cache."""
     b = Batch(zha, [40000, 7, 20000], 2, 4, 64, 16, BF, F32, seed=17)

@@ -309,3 +309,22 @@ def test_caches_refuse_other_element_types(zha, dtype):
         zha.page_pool(x, x, table, _OnGpu(torch.zeros(6, dtype=torch.int32)))
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         zha.kv_batch(_OnGpu(torch.zeros(2, 4, 9, 128, dtype=dtype)), _OnGpu(torch.zeros(2, 4, 9, 128, dtype=dtype)))
+
+
+def test_attend_batch_refuses_an_output_that_overlaps_the_queries(zha):
+    """A unit's output would be written over queries that another unit still reads."""
+    cfg = _cfg(zha)
+    before = zha.launch_count()
+    ws = zha.attend_batch_workspace_bytes(cfg, 4, 1000)
+    kv = _kv(zha)
+    for dt, elt in ((0, 4), (1, 2)):
+        size = 4 * 32 * 128 * elt
+        for shift in (16, size // 2, size - 16, -16, 16 - size):
+            rc = zha.lib.zha_attend_batch_kv(ctypes.byref(cfg), 1 << 43, dt, ctypes.byref(kv), 4, 1 << 44, 1000,
+                                             (1 << 43) + shift, None, 1 << 46, ws, None, None)
+            assert rc == zha.ZHA_ERR_INVALID and "overlaps" in zha.last_error(), (dt, shift)
+        for shift in (size, -size, 0):                       # beside it, or it: the next check answers
+            rc = zha.lib.zha_attend_batch_kv(ctypes.byref(cfg), 1 << 43, dt, ctypes.byref(kv), 4, 1 << 44, 1000,
+                                             (1 << 43) + shift, None, None, ws, None, None)
+            assert rc == zha.ZHA_ERR_CAPACITY, (dt, shift)
+    assert zha.launch_count() == before
