@@ -497,8 +497,8 @@ zha_status zha_rope_init(const zha_rope_spec* c, zha_rope* out) {
   if (banded && !(c->original_tokens > 0 && std::isfinite(c->original_tokens) && c->low > 0 && c->high > c->low &&
                   std::isfinite(c->high)))
     return rope_fail(ZHA_ERR_INVALID, "zha_rope_init: need original_tokens > 0 and 0 < low < high");
-  if (!(c->amplitude >= 0.0) || !std::isfinite(c->amplitude))
-    return rope_fail(ZHA_ERR_INVALID, "zha_rope_init: amplitude must be finite and >= 0");
+  if (!(c->amplitude >= 0.0) || !std::isfinite(float(c->amplitude)) || (c->amplitude > 0.0 && float(c->amplitude) == 0.f))
+    return rope_fail(ZHA_ERR_INVALID, "zha_rope_init: amplitude must be >= 0 and in the range of float32");
   const double two_pi = 6.283185307179586476925286766559;
   double base = c->base;
   if (c->scaling == ZHA_ROPE_NTK && D > 2) base *= std::pow(f, double(D) / (D - 2));

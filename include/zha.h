@@ -363,7 +363,7 @@ typedef struct {
     double factor;           /* >= 1, read unless PLAIN */
     double original_tokens;  /* > 0, read by YARN and BANDS */
     double low, high;        /* 0 < low < high, read by YARN and BANDS */
-    double amplitude;        /* A, >= 0; 0: 1 (YARN: 0.1 ln(factor) + 1) */
+    double amplitude;        /* A, >= 0, in the range of float32; 0: 1 (YARN: 0.1 ln(factor) + 1) */
 } zha_rope_spec;
 
 /* A rotation ready for use: plain host data, filled by zha_rope_init. */

@@ -328,3 +328,11 @@ def test_attend_batch_refuses_an_output_that_overlaps_the_queries(zha):
                                              (1 << 43) + shift, None, None, ws, None, None)
             assert rc == zha.ZHA_ERR_CAPACITY, (dt, shift)
     assert zha.launch_count() == before
+
+
+@pytest.mark.parametrize("amplitude", [1e39, 1e308, 1e-60])
+def test_rope_init_refuses_amplitudes_that_float32_does_not_hold(zha, amplitude):
+    """They became infinity, or 0, in the table, and the turned rows with them."""
+    with pytest.raises(zha.ZhaError):
+        zha.Rope(64, amplitude=amplitude)
+    assert zha.Rope(64, amplitude=3e38).table.amplitude > 2.9e38 and zha.Rope(64, amplitude=1e-40).table.amplitude > 0
