@@ -22,10 +22,12 @@
 // A second kernel finds a unit's pieces from the tile counts alone and joins them in a
 // fixed order.
 //
-// Products. A unit has at most 16 query heads, an eighth of a tcgen05 tile, and the
-// call is bound by the cache it reads and, when it runs for long, by the power that the
-// products take: the warps' own matrix instructions (16 x 8 x 16 bf16, 16 x 8 x 8 tf32)
-// take their operands from the warp's registers and tile without a hand-over. Keys
+// Products. Up to 8 query heads a KV head the call is bound by the cache it reads and, when
+// it runs for long, by the power that the products take: the warps' own matrix
+// instructions (16 x 8 x 16 bf16, 16 x 8 x 8 tf32) take their operands from the warp's
+// registers and tile without a hand-over. With 9 to 16 heads it is bound by the issue of these
+// instructions, which is this choice's limit and not the hardware's (keys as the M of a tcgen05
+// instruction would take them); beyond 16 the cache is read once per 16 heads. Keys
 // and elements of V are their 16 rows, heads their 8 columns, so that no row is padding:
 // S^T = K Q^T, O^T = V^T P^T. With up to 4 heads the columns hold two terms of the
 // fp32 operand side by side.
@@ -36,7 +38,7 @@
 //   weight times value the product of the two second terms (2^-11 of the weight, 2^-10
 //   of the value) is left out where it would take an instruction of its own.
 // Measured (held for half a second; the copy rate is 6.55 TB/s): 1M bf16 tokens of 4 KV
-// heads with 8 fp32 query heads each in 327 to 346 us by GPU (6.2 to 6.57 TB/s); 8
+// heads with 8 fp32 query heads each in 321 to 347 us by GPU (6.2 to 6.57 TB/s); 8
 // sequences up to 32K of 8 KV heads, 4 bf16 query heads each, in 98 to 102 us (91 to 94%);
 // 160 ragged ones up to 3001 in 90 us (80%). A call starts to read after 3 us, and the
 // join takes 3 to 4 us, whatever the length. One bulk copy per row instead of 16 cp.async
@@ -63,8 +65,8 @@ constexpr int kMaxWarps = kMaxCtas * kWarps;
 // CTAs as in the first: 105 and 95; a sixteenth to half as many 102 and 93.
 constexpr int kTwoTiers = 24;
 // What a unit's start and end cost, in tiles: the deal counts them, so that a warp with
-// many short units has fewer tiles (238 sequences up to 255 tokens of 8 KV heads: 33.7 us,
-// 53.5 without; 1 37.2, 5 34.7).
+// many short units has fewer tiles (238 sequences up to 255 tokens of 8 KV heads, with their
+// caches partly in L2: 33.7 us, 53.5 without; 1 37.2, 5 34.7; from HBM 40).
 constexpr int kUnitCost = 2;
 constexpr int kMinTiles = 2;            // no warp takes less, unless there is less
 // Up to so many tiles a unit, and no more units than CTAs at a time, a CTA takes a

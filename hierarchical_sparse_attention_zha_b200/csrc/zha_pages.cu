@@ -12,12 +12,16 @@
 //   3  entries and counts, with every rank known
 // What moves page contents is wide: a second launch over the whole GPU, unless it is
 // small enough to be done by the cluster.
-// Bound: the launch and the passes' latencies (about 12 dependent accesses of 0.6 us);
-// the copied rows (HBM) for compact. Measured: free, fork and extend of a beam of 4 in
-// 18 us on the device together; 48 forks of 128 sequences in 8 x 8300 pages, and all
-// of them extended, in 34 us; 7,300 pages of 32 KB moved in 79 us (6.1 TB/s of reads and
-// writes). As three launches over the whole GPU each, extend and fork took the same
-// time on the device and 9 us more on the host.
+// Bound: for small lists the launch and the passes' latencies (about 12 dependent accesses of
+// 0.6 us: 7 us); for large ones the work of the cluster, which is at most 16 of 148 SMs: extend
+// checks every block of every sequence, every CTA ranks every row and reads the needs of all
+// of its item's heads, the search for duplicates walks the list once per row, and the fork's copy costs
+// its instance 160 bytes of spills. The copied rows (HBM) for compact. Measured, by kernel: 48 forks of
+// 128 sequences of up to 4096 tokens in 8 heads 16 us and their copies 8, all 128 extended 18; 384 forks of
+// 1024 sequences 57 and 14, all extended 93; 1500 of 4000 with 2 heads 65 and 14, 121. Free, fork
+// and extend of a beam of 4: 18 us on the device together; 7,300 pages of 32 KB moved in 79 us
+// (6.1 TB/s of reads and writes). As three launches over the whole GPU each, extend and
+// fork of the 128 took the same time on the device and 9 us more on the host.
 #include <cstdio>
 
 #include "zha_host.cuh"

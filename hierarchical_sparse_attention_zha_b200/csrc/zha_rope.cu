@@ -38,7 +38,9 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeTokens = 32;          // a block, at most
-constexpr int kRopeTarget = 192;         // rows a block (96: 16K tokens 81 us, 32K rows 85; 192: 76, 86; 384: 77, 90)
+// Rows a block. In one run each, inputs partly in L2: 96: 16K tokens 81 us, 32K rows 84; 192: 76, 85; 384:
+// 76, 89. 200K tokens of 4 rows: 130, 125, 125.
+constexpr int kRopeTarget = 192;
 
 struct RopeTable {
   int32_t pairs;               // 0: nothing is turned
