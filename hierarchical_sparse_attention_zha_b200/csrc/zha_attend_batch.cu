@@ -1103,6 +1103,8 @@ zha_status zha_attend_batch_kv(const zha_config* cfg, const void* d_Q, int32_t q
   if (q_dtype != ZHA_F32 && q_dtype != ZHA_BF16)
     return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: unknown q_dtype");
   if (d_n_tokens == nullptr) return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: n_tokens is NULL");
+  if (!zha_may_lie(d_n_tokens) || !zha_may_lie(d_lse) || !zha_may_lie(d_status))
+    return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: n_tokens, lse or status at no multiple of its type's size");
   const uintptr_t q0 = reinterpret_cast<uintptr_t>(d_Q), o0 = reinterpret_cast<uintptr_t>(d_O);
   if (q0 != o0 && (q0 < o0 ? o0 - q0 : q0 - o0) < uint64_t(n_seqs) * G.hq * G.d * (q_dtype == ZHA_F32 ? 4 : 2))
     return zha_report_error(ZHA_ERR_INVALID, "zha_attend_batch_kv: O overlaps Q without being Q");

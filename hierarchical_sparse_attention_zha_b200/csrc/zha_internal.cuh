@@ -384,3 +384,6 @@ zha_status zha_geometry(const zha_config* cfg, zha::Geom* g);
 zha_status zha_batch_view(const zha::Geom& g, const zha_kv_cache* kv, int32_t n_seqs, int64_t max_tokens,
                           const char* who, zha::KvView* out);
 zha_status zha_report_cuda(cudaError_t e, const char* who);
+// Whether an array of T may lie at p (NULL: one that is left out).
+template <typename T>
+inline bool zha_may_lie(const T* p) { return reinterpret_cast<uintptr_t>(p) % sizeof(T) == 0; }

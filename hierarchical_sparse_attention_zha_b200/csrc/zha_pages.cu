@@ -529,6 +529,11 @@ zha_status need_ws(void* d_ws, size_t have, int64_t need) {
 
 constexpr int64_t kMaxItemRows = int64_t(1) << 24;
 
+zha_status words_ok(const int32_t* a, const int32_t* b, const int64_t* c, const int32_t* status) {
+  if (zha_may_lie(a) && zha_may_lie(b) && zha_may_lie(c) && zha_may_lie(status)) return ZHA_OK;
+  return zha_report_error(ZHA_ERR_INVALID, "zha_pages: a list, output or status at no multiple of its type's size");
+}
+
 zha_status items_ok(const PoolArgs& P, int32_t n_items, const void* a, const void* b, const char* what) {
   if (n_items < 0 || n_items > 65535 || int64_t(n_items) * P.hkv > kMaxItemRows)
     return zha_report_error(ZHA_ERR_INVALID, what);
@@ -623,6 +628,7 @@ zha_status zha_pages_extend(const zha_config* cfg, const zha_page_pool* pool, co
   if ((st = zha::items_ok(P, n_items, d_seqs, d_n_tokens,
                           "zha_pages_extend: n_items out of range, or seqs or n_tokens NULL")) != ZHA_OK || n_items == 0)
     return st;
+  if ((st = zha::words_ok(d_seqs, nullptr, d_n_tokens, d_status)) != ZHA_OK) return st;
   P.status = d_status;
   return zha::run_items<false>(P, nullptr, d_seqs, d_n_tokens, n_items, d_ws, ws_bytes,
                                static_cast<cudaStream_t>(stream), "zha_pages_extend");
@@ -638,6 +644,7 @@ zha_status zha_pages_fork(const zha_config* cfg, const zha_page_pool* pool, cons
                           "zha_pages_fork: n_items out of range, or dst or n_tokens NULL")) != ZHA_OK || n_items == 0)
     return st;
   if (d_src == nullptr) return zha_report_error(ZHA_ERR_INVALID, "zha_pages_fork: src is NULL");
+  if ((st = zha::words_ok(d_src, d_dst, d_n_tokens, d_status)) != ZHA_OK) return st;
   P.status = d_status;
   return zha::run_items<true>(P, d_src, d_dst, d_n_tokens, n_items, d_ws, ws_bytes, static_cast<cudaStream_t>(stream),
                               "zha_pages_fork");
@@ -651,6 +658,7 @@ zha_status zha_pages_free(const zha_config* cfg, const zha_page_pool* pool, cons
   if ((st = zha::items_ok(P, n_items, d_seqs, d_seqs,
                           "zha_pages_free: n_items out of range, or seqs NULL")) != ZHA_OK || n_items == 0)
     return st;
+  if ((st = zha::words_ok(d_seqs, nullptr, d_keep, d_status)) != ZHA_OK) return st;
   P.status = d_status;
   return zha::launch_page_kernel("pages_free_kernel", "zha_pages_free", zha::pages_free_kernel,
                                  int64_t(n_items) * P.hkv, static_cast<cudaStream_t>(stream), P, d_seqs, d_keep);
@@ -662,6 +670,7 @@ zha_status zha_pages_compact(const zha_config* cfg, const zha_page_pool* pool, i
   const char* who = "zha_pages_compact";
   zha_status st = zha::pool_args(cfg, pool, who, &P);
   if (st != ZHA_OK) return st;
+  if ((st = zha::words_ok(d_page_map, d_n_live, nullptr, d_status)) != ZHA_OK) return st;
   P.status = d_status;
   const zha::PageWs W = zha::page_ws(d_ws, P.n_pages, 0);
   if ((st = zha::need_ws(d_ws, ws_bytes, W.bytes)) != ZHA_OK) return st;

@@ -551,6 +551,8 @@ zha_status zha_rope_apply(const zha_rope* rope, const zha_rows* x, int32_t x_dty
     return rope_fail(ZHA_ERR_INVALID,
                      "zha_rope_apply: rows and positions must be non-NULL, rows 16-byte aligned with strides of "
                      "whole 16-byte pieces");
+  if (!zha_may_lie(d_pos))
+    return rope_fail(ZHA_ERR_INVALID, "zha_rope_apply: positions at no multiple of 8 bytes");
   if (x->data == y->data &&
       (x_dtype != y_dtype || x->token_stride != y->token_stride || x->head_stride != y->head_stride))
     return rope_fail(ZHA_ERR_INVALID, "zha_rope_apply: in place, both sides need one type and one set of strides");
@@ -600,6 +602,8 @@ zha_status zha_rope_append_kv(const zha_config* cfg, const zha_rope* rope, const
     return rope_fail(ZHA_ERR_INVALID, "zha_rope_append_kv: q_out must be a non-NULL 16-byte aligned device pointer");
   if (d_seq == nullptr || d_index == nullptr)
     return rope_fail(ZHA_ERR_INVALID, "zha_rope_append_kv: seq and index must be non-NULL");
+  if (!zha_may_lie(d_seq) || !zha_may_lie(d_index) || !zha_may_lie(d_pos) || !zha_may_lie(d_status))
+    return rope_fail(ZHA_ERR_INVALID, "zha_rope_append_kv: seq, index, positions or status at no multiple of its type's size");
   const zha::RopeTable R = zha::table_of(rope);
   RowSet Q{}, K{}, V{};
   if (q != nullptr) Q = RowSet{q->data, d_q_out, q->token_stride, q->head_stride, int64_t(G.hq) * G.d, G.d, G.hq};

@@ -322,7 +322,8 @@ zha_status zha_sparse_attend_kv(const zha_tree* tree, const float* d_Q, const zh
  * element s * n_kv_heads * ld * head_dim), as the tree's calls take it. Of the
  * zha_config they read the head counts, head_dim, chunk and kv_dtype; rope_pairs
  * and the tree's own fields must be valid but play no part. At most 2^31 - 512 token
- * slots per pool and 65535 sequences. */
+ * slots per pool and 65535 sequences. Arrays lie at multiples of their type's size, or
+ * of what a call says; others are refused (ZHA_ERR_INVALID). */
 
 /* ---- Rotary positions [Attention: "Attention 은 순서를 모르므로 위치 정보를 따로
  * 넣는다"] ------------------------------------------------------------------------

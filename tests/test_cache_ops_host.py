@@ -336,3 +336,48 @@ def test_rope_init_refuses_amplitudes_that_float32_does_not_hold(zha, amplitude)
     with pytest.raises(zha.ZhaError):
         zha.Rope(64, amplitude=amplitude)
     assert zha.Rope(64, amplitude=3e38).table.amplitude > 2.9e38 and zha.Rope(64, amplitude=1e-40).table.amplitude > 0
+
+
+def test_batch_calls_refuse_words_between_their_addresses(zha):
+    """An access there would be an error of the GPU's; the host refuses the call. The workspace's
+    answer comes after it, and shows that the same call with good addresses passes."""
+    cfg, rope, before = _cfg(zha), zha.Rope(128), zha.launch_count()
+    b, L, kv = ctypes.byref, zha.lib, _kv(zha)
+    inv, cap = zha.ZHA_ERR_INVALID, zha.ZHA_ERR_CAPACITY
+    rows = lambda at: b(zha.Rows(at, 512, 128))
+    pool = zha.PagePool(1 << 40, 1 << 41, 500, 1 << 42, 16, 1 << 43, 8, 0)
+    at = {k: 1 << (44 + i) for i, k in enumerate(("n", "lse", "status", "seq", "index", "pos", "dst"))}
+
+    def attend(n, lse, status):
+        return L.zha_attend_batch_kv(b(cfg), 1 << 52, 0, b(kv), 4, n, 1000, 1 << 53, lse, None, 0, status, None)
+
+    def append(seq, index, pos, status):
+        return L.zha_rope_append_kv(b(cfg), b(rope.table), None, rows(1 << 52), rows(1 << 53), 1, 3, b(kv), 2, seq, index,
+                                    pos, None, 0, status, None)
+
+    def extend(seq, n, status):
+        return L.zha_pages_extend(b(cfg), b(pool), seq, n, 8, None, 0, status, None)
+
+    def fork(seq, dst, n, status):
+        return L.zha_pages_fork(b(cfg), b(pool), seq, dst, n, 8, None, 0, status, None)
+
+    def free(seq, n, status):
+        return L.zha_pages_free(b(cfg), b(pool), seq, n, 8, status, None)
+
+    def compact(dst, n, status):
+        return L.zha_pages_compact(b(cfg), b(pool), dst, n, None, 0, status, None)
+
+    def turn(pos):
+        return L.zha_rope_apply(b(rope.table), rows(1 << 52), 1, pos, 5, 4, 0, rows(1 << 53), 1, None)
+
+    for call, names, answer in ((attend, ("n", "lse", "status"), cap), (append, ("seq", "index", "pos", "status"), None),
+                                (extend, ("seq", "n", "status"), cap), (fork, ("seq", "dst", "n", "status"), cap),
+                                (free, ("seq", "n", "status"), None), (compact, ("dst", "n", "status"), cap),
+                                (turn, ("pos",), None)):
+        good = [at[k] for k in names]
+        if answer is not None:
+            assert call(*good) == answer, call.__name__
+        for i, k in enumerate(names):
+            for shift in (1, 2, 4) if k in ("index", "pos") or (k == "n" and call is not compact) else (1, 2, 3):
+                assert call(*good[:i], good[i] + shift, *good[i + 1:]) == inv, (call.__name__, k, shift)
+    assert zha.launch_count() == before
